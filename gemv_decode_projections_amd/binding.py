@@ -25,6 +25,8 @@ STATUS = {
     -7: "PROJ_ERR_HIP",
     -8: "PROJ_ERR_DEVICE",
     -9: "PROJ_ERR_SCRATCH",
+    -10: "PROJ_ERR_ARG",
+    -11: "PROJ_ERR_PAGES",
 }
 
 

@@ -28,6 +28,8 @@ SOURCES = [
     "rowdot_variants.hip",
     "wide_variants.hip",
     "wide_dma_variants.hip",
+    "attn.hip",
+    "attn_rows.hip",
 ]
 
 ARCH = os.environ.get("GDP_OFFLOAD_ARCH", "gfx950")

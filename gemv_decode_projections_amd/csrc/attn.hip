@@ -1,0 +1,305 @@
+// C ABI of the paged cache and the attention over it (include/block.h):
+// checks, the choice of the kernel, launches; and the two cache kernels.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "attn.h"
+
+namespace gdp {
+namespace {
+
+// One 16-byte piece of a new token's key or value per thread: a pure copy,
+// bound by the launch at decode sizes and by HBM at a prompt's.
+__global__ __launch_bounds__(256) void kv_append_kernel(AttnArgs a, const char *kin, const char *vin, int64_t in_stride,
+                                                        int64_t in_head, int per_head, int per_token, int64_t total)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= total)
+        return;
+    const int tok = (int)(id / per_token);
+    const int piece = (int)(id - (int64_t)tok * per_token);
+    const int head = piece / per_head;
+    const int at = (piece - head * per_head) * 16;
+    // The token's sequence: the last whose first row is not past it.
+    int lo = 0, hi = a.seqs;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.q_start[mid] <= tok)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    if (lo >= a.seqs)
+        return;
+    int tok0, n, len;
+    seq_bounds(a, lo, tok0, n, len);
+    const int pos = len - n + tok - tok0;
+    if (tok < tok0 || tok >= tok0 + n || pos < 0)
+        return;
+    int64_t off;
+    if (!kv_offset(a, a.table[lo * a.table_stride + (pos >> a.page_shift)], pos, (int64_t)head * a.head_stride, off))
+        return;
+    const int64_t from = tok * in_stride + head * in_head + at;
+    const u32x4 k = *reinterpret_cast<const u32x4 *>(kin + from);
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(vin + from);
+    *reinterpret_cast<u32x4 *>(const_cast<char *>(a.k) + off + at) = k;
+    *reinterpret_cast<u32x4 *>(const_cast<char *>(a.v) + off + at) = v;
+}
+
+// Page pairs travel in the kernel's arguments: no device list to allocate,
+// copy or keep alive, and a graph keeps its own.
+constexpr int kPairs = 448;
+struct CopyArgs {
+    char *k, *v;
+    int64_t page_stride;       // bytes
+    int page_bytes;
+    int32_t src[kPairs], dst[kPairs];
+};
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;         // 16-byte pieces per thread, all loads in flight
+
+__global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(CopyArgs a)
+{
+    char *base = blockIdx.z ? a.v : a.k;
+    const char *src = base + a.src[blockIdx.y] * a.page_stride;
+    char *dst = base + a.dst[blockIdx.y] * a.page_stride;
+    const int at = (blockIdx.x * kCopyThreads * kCopyUnroll + threadIdx.x) * 16;
+    u32x4 x[kCopyUnroll];
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+        if (at + i * kCopyThreads * 16 < a.page_bytes)
+            x[i] = *reinterpret_cast<const u32x4 *>(src + at + i * kCopyThreads * 16);
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+        if (at + i * kCopyThreads * 16 < a.page_bytes)
+            *reinterpret_cast<u32x4 *>(dst + at + i * kCopyThreads * 16) = x[i];
+}
+
+constexpr int64_t kMaxOffset = (int64_t)1 << 31;
+
+bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < ((int64_t)1 << 40); }
+
+int check_cache(const blk_cache *c)
+{
+    if (!c || !c->k || !c->v)
+        return PROJ_ERR_NULL;
+    if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16))
+        return PROJ_ERR_ALIGN;
+    if (c->dtype != BLK_BF16 && c->dtype != BLK_F16)
+        return PROJ_ERR_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return PROJ_ERR_ARG;
+    if (c->n_pages < 1 || c->kv_heads < 1 || c->kv_heads > 65535 || c->page_size < 4 ||
+        (c->page_size & (c->page_size - 1)))
+        return PROJ_ERR_ARG;
+    if (!stride_ok(c->page_stride) || !stride_ok(c->token_stride) || !stride_ok(c->head_stride) ||
+        c->page_stride >= kMaxOffset || c->token_stride >= kMaxOffset / 2 || c->head_stride >= kMaxOffset / 2 ||
+        (c->page_size - 1) * c->token_stride + (c->kv_heads - 1) * c->head_stride + c->head_dim > kMaxOffset)
+        return PROJ_ERR_ARG;
+    return PROJ_OK;
+}
+
+int check_batch(const blk_batch *b)
+{
+    if (!b)
+        return PROJ_ERR_NULL;
+    if (b->seqs < 0 || b->tokens < 0 || b->table_width < 1 || b->table_stride < b->table_width)
+        return PROJ_ERR_ARG;
+    if (b->seqs && b->tokens && (!b->q_start || !b->kv_len || !b->table))
+        return PROJ_ERR_NULL;
+    if (!aligned_to(b->q_start, 4) || !aligned_to(b->kv_len, 4) || !aligned_to(b->table, 4))
+        return PROJ_ERR_ALIGN;
+    return PROJ_OK;
+}
+
+AttnArgs base_args(const blk_cache *c, const blk_batch *b)
+{
+    AttnArgs a{};
+    a.k = static_cast<const char *>(c->k);
+    a.v = static_cast<const char *>(c->v);
+    a.page_stride = (uint32_t)(c->page_stride * 2);
+    a.token_stride = (int)(c->token_stride * 2);
+    a.head_stride = (int)(c->head_stride * 2);
+    a.n_pages = c->n_pages;
+    a.page_shift = __builtin_ctz((unsigned)c->page_size);
+    a.page_mask = c->page_size - 1;
+    a.kv_heads = c->kv_heads;
+    a.q_start = b->q_start;
+    a.kv_len = b->kv_len;
+    a.table = b->table;
+    a.table_stride = b->table_stride;
+    a.table_width = b->table_width;
+    a.seqs = b->seqs;
+    a.tokens = b->tokens;
+    return a;
+}
+
+int launch(const void *fn, dim3 grid, dim3 block, void *arg, void *stream)
+{
+    void *params[1] = {arg};
+    const hipError_t e = hipLaunchKernel(fn, grid, block, params, 0, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? PROJ_OK : hip_fail(e);
+}
+
+}  // namespace
+}  // namespace gdp
+
+using namespace gdp;
+
+extern "C" {
+
+int blk_kv_append(const blk_cache *cache, const blk_batch *batch, const void *k, const void *v, int64_t in_stride,
+                  int64_t in_head_stride, void *stream)
+{
+    int rc = check_cache(cache);
+    if (rc == PROJ_OK)
+        rc = check_batch(batch);
+    if (rc)
+        return rc;
+    if (!stride_ok(in_stride) || !stride_ok(in_head_stride))
+        return PROJ_ERR_ARG;
+    if (!batch->seqs || !batch->tokens)
+        return PROJ_OK;
+    if (!k || !v)
+        return PROJ_ERR_NULL;
+    if (!aligned_to(k, 16) || !aligned_to(v, 16))
+        return PROJ_ERR_ALIGN;
+    AttnArgs a = base_args(cache, batch);
+    int per_head = cache->head_dim / 8, per_token = per_head * cache->kv_heads;
+    int64_t total = (int64_t)batch->tokens * per_token;
+    if ((total + 255) / 256 > 0x7fffffff)
+        return PROJ_ERR_ARG;
+    const char *kin = static_cast<const char *>(k), *vin = static_cast<const char *>(v);
+    int64_t stride = in_stride * 2, head = in_head_stride * 2;
+    hipLaunchKernelGGL(kv_append_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), a, kin, vin, stride, head, per_head, per_token, total);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? PROJ_OK : hip_fail(e);
+}
+
+int blk_kv_copy_pages(const blk_cache *cache, const int32_t *src, const int32_t *dst, int n, void *stream)
+{
+    const int rc = check_cache(cache);
+    if (rc)
+        return rc;
+    if (n < 0)
+        return PROJ_ERR_ARG;
+    if (n == 0)
+        return PROJ_OK;
+    if (!src || !dst)
+        return PROJ_ERR_NULL;
+    // One dense block per page: the two inner strides are the two ways to
+    // order tokens and heads.
+    const int64_t elems = (int64_t)cache->page_size * cache->kv_heads * cache->head_dim;
+    const bool token_major = (cache->head_stride == cache->head_dim || cache->kv_heads == 1) &&
+                             cache->token_stride == (int64_t)cache->kv_heads * cache->head_dim;
+    const bool head_major = cache->token_stride == cache->head_dim &&
+                            (cache->head_stride == (int64_t)cache->page_size * cache->head_dim || cache->kv_heads == 1);
+    if (!(token_major || head_major) || elems * 2 > (1 << 30) || (cache->n_pages > 1 && cache->page_stride < elems))
+        return PROJ_ERR_ARG;
+    try {
+        // A page is written once at most, and none both read and written.
+        std::vector<uint8_t> use(cache->n_pages, 0);
+        for (int i = 0; i < n; ++i) {
+            if (src[i] < 0 || src[i] >= cache->n_pages || dst[i] < 0 || dst[i] >= cache->n_pages || (use[dst[i]] & 2))
+                return PROJ_ERR_ARG;
+            use[src[i]] |= 1;
+            use[dst[i]] |= 2;
+        }
+        for (int i = 0; i < n; ++i)
+            if (use[dst[i]] & 1)
+                return PROJ_ERR_ARG;
+    } catch (const std::bad_alloc &) {
+        return PROJ_ERR_HIP;
+    }
+    CopyArgs a{};
+    a.k = static_cast<char *>(cache->k);
+    a.v = static_cast<char *>(cache->v);
+    a.page_stride = cache->page_stride * 2;
+    a.page_bytes = (int)(elems * 2);
+    const unsigned per_page = (unsigned)((a.page_bytes + kCopyThreads * kCopyUnroll * 16 - 1) / (kCopyThreads * kCopyUnroll * 16));
+    for (int i = 0; i < n; i += kPairs) {
+        const int c = std::min(kPairs, n - i);
+        memcpy(a.src, src + i, c * sizeof(int32_t));
+        memcpy(a.dst, dst + i, c * sizeof(int32_t));
+        const int rc2 = launch(reinterpret_cast<const void *>(kv_copy_kernel), dim3(per_page, c, 2),
+                               dim3(kCopyThreads), &a, stream);
+        if (rc2)
+            return rc2;
+    }
+    return PROJ_OK;
+}
+
+size_t blk_attn_workspace_bytes(int head_dim) { return head_dim > 0 && head_dim <= 256 ? attn_ws_bytes(head_dim) : 0; }
+
+int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_args *args, void *ws, size_t ws_bytes,
+                 void *stream)
+{
+    int rc = check_cache(cache);
+    if (rc == PROJ_OK)
+        rc = check_batch(batch);
+    if (rc)
+        return rc;
+    if (!args)
+        return PROJ_ERR_NULL;
+    if (args->heads < 1 || args->heads % cache->kv_heads || args->max_q < 1 || args->window < 0 ||
+        !(args->scale > 0.f) || !isfinite(args->scale))
+        return PROJ_ERR_ARG;
+    for (int64_t s : {args->q_stride, args->q_head_stride, args->gate_stride, args->gate_head_stride, args->out_stride,
+                      args->out_head_stride})
+        if (!stride_ok(s))
+            return PROJ_ERR_ARG;
+    if (!batch->seqs || !batch->tokens)
+        return PROJ_OK;
+    if (!args->q || !args->out || !ws)
+        return PROJ_ERR_NULL;
+    if (!aligned_to(args->q, 16) || !aligned_to(args->out, 16) || !aligned_to(args->gate, 16) ||
+        !aligned_to(args->lse, 4) || !aligned_to(ws, 256))
+        return PROJ_ERR_ALIGN;
+    if (ws_bytes < attn_ws_bytes(cache->head_dim))
+        return PROJ_ERR_SCRATCH;
+    // Row counts, positions and tile counts are kept in 32 bits.
+    const int64_t rows = (int64_t)batch->tokens * (args->heads / cache->kv_heads);
+    if (rows > 0x3fffffff || ((int64_t)batch->table_width << __builtin_ctz((unsigned)cache->page_size)) > 0x3fffffff)
+        return PROJ_ERR_ARG;
+
+    AttnArgs a = base_args(cache, batch);
+    a.q = static_cast<const char *>(args->q);
+    a.gate = static_cast<const char *>(args->gate);
+    a.out = static_cast<char *>(args->out);
+    a.lse = args->lse;
+    a.q_stride = args->q_stride * 2;
+    a.q_head = args->q_head_stride * 2;
+    a.gate_stride = args->gate_stride * 2;
+    a.gate_head = args->gate_head_stride * 2;
+    a.out_stride = args->out_stride * 2;
+    a.out_head = args->out_head_stride * 2;
+    a.heads = args->heads;
+    a.group = args->heads / cache->kv_heads;
+    a.window = std::min(args->window, 0x3fffffff);
+    a.scale_log2 = args->scale * 1.44269504f;
+    a.counters = static_cast<uint32_t *>(ws);
+    a.slots = static_cast<char *>(ws) + kAttnCounterBytes;
+
+    const int64_t seq_rows = (int64_t)std::min(args->max_q, batch->tokens) * a.group;
+    const int nb = seq_rows <= 16 ? 1 : seq_rows <= 32 || cache->head_dim == 256 ? 2 : 4;
+    const int tile = 16 * nb;
+    const void *fn = reinterpret_cast<const void *>(attn_rows_kernel(cache->dtype, cache->head_dim, nb));
+    a.kv_step = 128;
+    a.min_split = 128;
+    a.target = attn_target(tile);
+    // Units: one per row tile and key head, and at most `target` more.
+    const int64_t tiles = (rows / tile + batch->seqs) * a.kv_heads;
+    const int64_t positions = (int64_t)batch->table_width * cache->page_size;
+    const int64_t grid = std::min(tiles + a.target, tiles * ((positions + a.min_split - 1) / a.min_split));
+    if (grid > 0x7fffffff)
+        return PROJ_ERR_ARG;
+    return launch(fn, dim3((unsigned)grid), dim3(256), &a, stream);
+}
+
+}  // extern "C"

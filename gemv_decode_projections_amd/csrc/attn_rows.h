@@ -1,0 +1,315 @@
+// Attention of few rows (up to 64 per tile: single tokens and drafted tokens)
+// over a paged cache. Memory bound: every key and value is read once, as long
+// as a sequence's rows fit one tile, and straight into registers.
+//
+// Mathematics, per tile of R = 16 NB rows and step of 32 positions, on
+// v_mfma 16x16x32 (geometry in common.h):
+//   S^T (32 x R) = K Q^T      A = keys (row l%16, elements 8(l/16)..+7 of each
+//                             32), B = the rows' queries;
+//   O^T (DIM x R) += V^T P^T  A = values transposed, B = P^T.
+// The score fragment of lane l holds column (row of the tile) l%16 and
+// positions 4(l/16) + i of each 16: the softmax of a row sits in four lanes,
+// and its eight probabilities are exactly the k slots of a B operand if A
+// uses the same order of positions, 4q..4q+3 and 16+4q..16+4q+3 for quad q.
+// So a lane reads those eight positions' values, VEC = 8 (4 for DIM 64)
+// consecutive elements each, 256 contiguous bytes per 16 lanes, and an
+// in-lane transposition (one byte permute per two elements) makes the VEC A
+// operands: operand j holds elements VEC * (l%16) + j. Nothing crosses LDS
+// until the four waves, which take every fourth step, join at the end.
+#pragma once
+
+#include "attn.h"
+
+namespace gdp {
+
+// Transposes 8 positions x VEC elements of 16 bits held by one lane into VEC
+// fragments of 8 positions: fragment j = element j of positions 0..7.
+template <int VEC>
+__device__ __forceinline__ void transpose8(const uint32_t (&in)[8][VEC / 2], u32x4 (&out)[VEC])
+{
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+            out[j][p] = __builtin_amdgcn_perm(in[2 * p + 1][j / 2], in[2 * p][j / 2],
+                                              j % 2 ? 0x07060302u : 0x05040100u);
+}
+
+// Two waves per SIMD where the accumulators leave room for them.
+template <class T, int DIM, int NB>
+__global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void attn_rows(AttnArgs a)
+{
+    constexpr int ROWS = 16 * NB;
+    constexpr int WAVES = 4;
+    constexpr int KS = DIM / 32;                     // k-steps of Q K^T
+    constexpr int VEC = DIM >= 128 ? 8 : DIM / 16;   // consecutive elements per lane and value row
+    constexpr int HALF = DIM / (16 * VEC);           // 16 * VEC element blocks of a value row
+    constexpr int PITCH = DIM + 4;
+    constexpr int STEP = 32;
+    __shared__ __align__(16) float s_o[ROWS * PITCH];
+    __shared__ float s_m[WAVES][ROWS], s_l[WAVES][ROWS];
+    __shared__ int s_flag;
+
+    AttnUnit u;
+    if (!find_unit<ROWS>(a, blockIdx.x, u))
+        return;
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int col = lane % 16, quad = lane / 16;
+
+    // The tile's queries as B operands; rows past the last read it again and
+    // see nothing.
+    u32x4 qf[NB][KS];
+    int see_lo[NB], see_hi[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int r = nb * 16 + col;
+        const int row = u.row0 + min(r, u.nrows - 1);
+        const int i = row / a.group;
+        const int head = u.kvh * a.group + row - i * a.group;
+        const char *p = a.q + (int64_t)(u.tok0 + i) * a.q_stride + head * a.q_head + quad * 16;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            qf[nb][ks] = *reinterpret_cast<const u32x4 *>(p + ks * 64);
+        const int pos = u.len - u.n + i;
+        see_hi[nb] = r < u.nrows ? pos + 1 : 0;
+        see_lo[nb] = a.window > 0 ? pos - a.window + 1 : 0;
+    }
+    // Positions that every row of the tile sees need no mask.
+    const int i0 = u.row0 / a.group, i1 = (u.row0 + u.nrows - 1) / a.group;
+    const int all_hi = u.len - u.n + i0 + 1;
+    const int all_lo = a.window > 0 ? u.len - u.n + i1 - a.window + 1 : 0;
+
+    f32x4 acc[NB][HALF][VEC];
+    float top[NB], sum[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        top[nb] = -INFINITY;
+        sum[nb] = 0.f;
+#pragma unroll
+        for (int h = 0; h < HALF; ++h)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                acc[nb][h][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t *table = a.table + (int64_t)u.seq * a.table_stride;
+    const int64_t head_off = (int64_t)u.kvh * a.head_stride;
+    auto page_of = [&](int p) { return table[min(p >> a.page_shift, a.table_width - 1)]; };
+    // Per step: the pages of the lane's two key rows and of its two groups of
+    // four value rows (four aligned positions share a page).
+    struct Pages {
+        int k[2], v[2];
+    };
+    auto load_pages = [&](int base) {
+        Pages pg;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            pg.k[t] = page_of(base + 16 * t + col);
+            pg.v[t] = page_of(base + 16 * t + 4 * quad);
+        }
+        return pg;
+    };
+    u32x4 kf[2][KS];
+    uint32_t vr[HALF][8][VEC / 2];
+    auto load_k = [&](int base, const Pages &pg) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            int64_t off;
+            kv_offset(a, pg.k[t], base + 16 * t + col, head_off, off);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                kf[t][ks] = *reinterpret_cast<const u32x4 *>(a.k + off + quad * 16 + ks * 64);
+        }
+    };
+    auto load_v = [&](int base, const Pages &pg) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            int64_t off;
+            kv_offset(a, pg.v[t], base + 16 * t + 4 * quad, head_off, off);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < HALF; ++h) {
+                    const char *p = a.v + off + (int64_t)i * a.token_stride + (h * 16 * VEC + col * VEC) * 2;
+                    if constexpr (VEC == 8) {
+                        const u32x4 x = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            vr[h][4 * t + i][e] = x[e];
+                    } else {
+                        const u32x2 x = *reinterpret_cast<const u32x2 *>(p);
+                        vr[h][4 * t + i][0] = x.x;
+                        vr[h][4 * t + i][1] = x.y;
+                    }
+                }
+        }
+    };
+
+    int base = u.lo + wave * STEP;
+    Pages pg = {}, next = {};
+    if (base < u.hi) {
+        pg = load_pages(base);
+        next = load_pages(base + WAVES * STEP);
+        load_k(base, pg);
+        load_v(base, pg);
+    }
+    for (; base < u.hi; base += WAVES * STEP) {
+        const int after = base + WAVES * STEP;
+        f32x4 s[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                s[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    s[nb][t] = T::mfma16(kf[t][ks], qf[nb][ks], s[nb][t]);
+            }
+        // The keys are in the scores: the next step's may take their registers.
+        const Pages coming = load_pages(min(after + WAVES * STEP, u.hi - 1));
+        if (after < u.hi)
+            load_k(after, next);
+        bool ok[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            ok[t] = (unsigned)pg.v[t] < (unsigned)a.n_pages;
+        const bool masked = base < all_lo || base + STEP > all_hi || base + STEP > u.hi || !__all(ok[0] && ok[1]);
+        if (masked) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int p = base + 16 * t + 4 * quad + i;
+                    const bool held = ok[t] && p < u.hi;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        if (!(held && p >= see_lo[nb] && p < see_hi[nb]))
+                            s[nb][t][i] = -INFINITY;
+                    // What lies past the last token is not the cache's: 0 * NaN.
+#pragma unroll
+                    for (int h = 0; h < HALF; ++h)
+#pragma unroll
+                        for (int e = 0; e < VEC / 2; ++e)
+                            vr[h][4 * t + i][e] = held ? vr[h][4 * t + i][e] : 0u;
+                }
+        }
+        u32x4 pf[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[nb][t][i] *= a.scale_log2;
+                    m = fmaxf(m, s[nb][t][i]);
+                }
+            m = fmaxf(top[nb], max_quads(m));
+            if (__any(m > top[nb])) {
+                const float f = exp2_fast(top[nb] - (m == -INFINITY ? 0.f : m));
+                top[nb] = m;
+                sum[nb] *= f;
+#pragma unroll
+                for (int h = 0; h < HALF; ++h)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        acc[nb][h][j] *= f;
+            }
+            const float safe = m == -INFINITY ? 0.f : m;
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                p[e] = exp2_fast(s[nb][e / 4][e % 4] - safe);
+                sum[nb] += p[e];
+            }
+            // Probabilities in 16 bits for the matrix instruction: each within
+            // half a unit of the type, errors that average out over a row;
+            // the sum keeps the unrounded ones.
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                pf[nb][e] = T::pack(p[2 * e], p[2 * e + 1]);
+        }
+#pragma unroll
+        for (int h = 0; h < HALF; ++h) {
+            u32x4 vt[VEC];
+            transpose8<VEC>(vr[h], vt);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    acc[nb][h][j] = T::mfma16(vt[j], pf[nb], acc[nb][h][j]);
+        }
+        if (after < u.hi)
+            load_v(after, next);
+        pg = next;
+        next = coming;
+    }
+
+    // Join the waves. Each scales its rows to the workgroup's maximum; then
+    // they add their parts into LDS in four turns, each turn a different
+    // quarter of the elements per wave.
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        sum[nb] = sum_quads(sum[nb]);
+        if (quad == 0) {
+            s_m[wave][nb * 16 + col] = top[nb];
+            s_l[wave][nb * 16 + col] = sum[nb];
+        }
+    }
+    __syncthreads();
+    float wm[NB], wl[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int r = nb * 16 + col;
+        float m = s_m[0][r];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w)
+            m = fmaxf(m, s_m[w][r]);
+        const float safe = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            l += s_l[w][r] * exp2_fast(s_m[w][r] - safe);
+        wm[nb] = m;
+        wl[nb] = l;
+        const float f = exp2_fast(top[nb] - safe);
+#pragma unroll
+        for (int h = 0; h < HALF; ++h)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                acc[nb][h][j] *= f;
+    }
+    for (int turn = 0; turn < WAVES; ++turn) {
+        const int mine = (wave + turn) % WAVES;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i != mine)
+                continue;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int h = 0; h < HALF; ++h)
+#pragma unroll
+                    for (int j = 0; j < VEC; j += 4) {
+                        f32x4 *p = reinterpret_cast<f32x4 *>(s_o + (nb * 16 + col) * PITCH + h * 16 * VEC +
+                                                             VEC * (4 * quad + i) + j);
+                        f32x4 x = {acc[nb][h][j][i], acc[nb][h][j + 1][i], acc[nb][h][j + 2][i], acc[nb][h][j + 3][i]};
+                        if (turn > 0)
+                            x += *p;
+                        *p = x;
+                    }
+        }
+        __syncthreads();
+    }
+    if (wave == 0 && quad == 0)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            s_m[0][nb * 16 + col] = wm[nb];
+            s_l[0][nb * 16 + col] = wl[nb];
+        }
+    __syncthreads();
+    leave_unit<T, DIM, ROWS, 256>(a, u, s_o, PITCH, s_m[0], s_l[0], &s_flag);
+}
+
+}  // namespace gdp

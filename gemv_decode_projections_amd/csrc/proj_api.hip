@@ -29,6 +29,16 @@ constexpr size_t kScratchBytes = kScratchPolled + kScratchCounted + kScratchCoun
 static __device__ __align__(256) unsigned char scratch[kScratchBytes];
 
 namespace gdp {
+
+static int g_last_hip = 0;
+
+// Shared with the block operators (block_common.h).
+int hip_fail(hipError_t e)
+{
+    g_last_hip = (int)e;
+    return PROJ_ERR_HIP;
+}
+
 namespace {
 
 struct LayerInfo {
@@ -99,17 +109,11 @@ struct LayerState {
 };
 
 LayerState g_layers[PROJ_NUM_LAYERS];
-int g_last_hip = 0;
 
 // Device address of `scratch` on each GPU (set once per device by prepare).
 constexpr int kMaxDevices = 64;
 void *g_scratch[kMaxDevices] = {};
 
-int hip_fail(hipError_t e)
-{
-    g_last_hip = (int)e;
-    return PROJ_ERR_HIP;
-}
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -1139,6 +1143,8 @@ const char *proj_strerror(int status)
     case PROJ_ERR_HIP: return "HIP runtime error";
     case PROJ_ERR_DEVICE: return "current device differs from the layer's device";
     case PROJ_ERR_SCRATCH: return "the plan's split-K partials exceed the fixed scratch of proj_run_noalloc";
+    case PROJ_ERR_ARG: return "a size, stride, type or index is outside what the operator takes";
+    case PROJ_ERR_PAGES: return "too few free pages in the pool";
     default: return "unknown status";
     }
 }
