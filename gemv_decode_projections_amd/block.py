@@ -38,6 +38,17 @@ class _Attn(ctypes.Structure):
                 ("heads", _i), ("max_q", _i), ("window", _i), ("scale", _f)]
 
 
+class _W4(ctypes.Structure):
+    _fields_ = [("n", _i), ("k", _i), ("group", _i), ("dtype", _i), ("has_zeros", _i)]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("x", _vp), ("residual", _vp), ("gate", _vp), ("weight_post", _vp), ("weight_pre", _vp),
+                ("residual_out", _vp), ("out", _vp), ("x_stride", _i64), ("residual_stride", _i64),
+                ("gate_stride", _i64), ("residual_out_stride", _i64), ("out_stride", _i64), ("width", _i),
+                ("dtype", _i), ("residual_dtype", _i), ("alpha", _f), ("eps", _f)]
+
+
 _FUNCS = None
 
 
@@ -52,6 +63,10 @@ def _lib():
             "blk_kv_copy_pages": ([cache, _vp, _vp, _i, _vp], _i),
             "blk_attn_run": ([cache, batch, ctypes.POINTER(_Attn), _vp, ctypes.c_size_t, _vp], _i),
             "blk_attn_workspace_bytes": ([_i], ctypes.c_size_t),
+            "blk_w4_packed_bytes": ([ctypes.POINTER(_W4)], ctypes.c_size_t),
+            "blk_w4_pack": ([ctypes.POINTER(_W4), _vp, _vp, _vp, _vp, _vp], _i),
+            "blk_w4_run": ([ctypes.POINTER(_W4), _vp, _vp, _i64, _i, _vp, _i64, _vp], _i),
+            "blk_norm_run": ([ctypes.POINTER(_Norm), _i, _vp], _i),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -196,3 +211,99 @@ def attn_run(q, cache, table, q_start, kv_len, out, ws, *, max_q=None, scale=Non
                  max(tokens, 1) if max_q is None else max_q, window, dim ** -0.5 if scale is None else scale)
     batch = _batch(cache, table, q_start, kv_len, tokens)
     _fail(_lib().blk_attn_run(cache._ref, batch, args, ws._ptr, ws.bytes, _raw_stream(stream, cache.device)), "attn_run")
+
+
+# ------------------------------------------------------------- 4-bit projections
+
+class W4Weight:
+    """A 4-bit weight matrix laid out for w4_run; made by w4_prepare."""
+
+    def __init__(self, shape, packed, dtype):
+        self.n, self.k, self.group = shape.n, shape.k, shape.group
+        self.packed, self.dtype, self.device = packed, dtype, packed.device
+        self._ref, self._ptr = ctypes.byref(shape), packed.data_ptr()
+        self._shape = shape
+
+
+def w4_prepare(q, scales, zeros=None, group=128):
+    """Lay out n x k 4-bit weights: q uint8 n x k/2 (element 2j in the low nibble of byte j), scales
+    n x k/group (BF16 or FP16, the type of the activations), zeros uint8 n x k/group of 0..15
+    (None: 8). Runs once and waits; the tensors may be freed afterwards."""
+    _need(q.dim() == 2 and q.dtype == torch.uint8 and q.is_contiguous() and q.is_cuda,
+          "q must be a contiguous uint8 device tensor n x k/2")
+    n, k = q.shape[0], 2 * q.shape[1]
+    _need(group in (32, 64, 128) and k % group == 0 and n >= 1 and k >= 1,
+          "group %s of k = %d: expected 32, 64 or 128, dividing k" % (group, k))
+    _need(scales.dtype in (torch.bfloat16, torch.float16) and scales.shape == (n, k // group) and scales.is_contiguous()
+          and scales.device == q.device, "scales must be a contiguous bfloat16 or float16 tensor %d x %d" % (n, k // group))
+    _need(zeros is None or (zeros.dtype == torch.uint8 and zeros.shape == scales.shape and zeros.is_contiguous()
+                            and zeros.device == q.device), "zeros must be a contiguous uint8 tensor %d x %d" % (n, k // group))
+    shape = _W4(n, k, group, DTYPES[scales.dtype], int(zeros is not None))
+    packed = torch.empty(_lib().blk_w4_packed_bytes(shape), dtype=torch.uint8, device=q.device)
+    stream = torch.cuda.current_stream(q.device)
+    _fail(_lib().blk_w4_pack(shape, q.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
+                             packed.data_ptr(), stream.cuda_stream), "w4_prepare")
+    stream.synchronize()
+    return W4Weight(shape, packed, scales.dtype)
+
+
+def w4_run(w, x, out, stream=None):
+    """out (m x n) = x (m x k) @ W^T with 4-bit weights; rows of x and out may be strided."""
+    if x.dtype != w.dtype or out.dtype != w.dtype or x.device != w.device or out.device != w.device:
+        raise ValueError("x is %s on %s, out %s on %s, the weights %s on %s"
+                         % (x.dtype, x.device, out.dtype, out.device, w.dtype, w.device))
+    m = x.shape[0]
+    if x.dim() != 2 or out.dim() != 2 or x.shape[1] != w.k or out.shape[0] != m or out.shape[1] != w.n:
+        raise ValueError("x has shape %s, out %s, expected m x %d and m x %d" % (tuple(x.shape), tuple(out.shape), w.k, w.n))
+    xs, os = x.stride(), out.stride()
+    if xs[1] != 1 or (os[1] != 1 and w.n > 1):
+        raise ValueError("the rows of x and out must be contiguous")
+    _fail(_lib().blk_w4_run(w._ref, w._ptr, x.data_ptr(), xs[0], m, out.data_ptr(), os[0],
+                            _raw_stream(stream, w.device)), "w4_run")
+
+
+# ------------------------------------------------------------- norms around a block
+
+def norm_run(x, residual, out, *, weight_pre, weight_post=None, gate=None, alpha=1.0, eps=1e-6, residual_out=None,
+             stream=None):
+    """residual_out = residual + alpha * gate * rms_norm(x, weight_post); out = rms_norm(residual_out, weight_pre).
+
+    x: a block's output (m x width), or None for the norm before the first block; residual: m x width
+    of x's type or float32; gate: width, or m x width; without weight_post x is added as it is.
+    residual_out defaults to residual, updated in place."""
+    _need(out.dim() == 2 and out.dtype in (torch.bfloat16, torch.float16) and out.is_cuda,
+          "out must be a bfloat16 or float16 device tensor m x width")
+    m, width = out.shape
+    dtype, device = out.dtype, out.device
+    _need(residual.dtype in (dtype, torch.float32), "residual has dtype %s, expected %s or float32" % (residual.dtype, dtype))
+    if x is None:
+        _need(weight_post is None and gate is None and residual_out is None, "weight_post, gate and residual_out need x")
+    elif residual_out is None:
+        residual_out = residual
+
+    def rows(what, t, kind):
+        if t is None:
+            return None, 0
+        if t.dtype != kind or t.device != device or t.shape != (m, width) or (t.stride(1) != 1 and width > 1):
+            raise ValueError("%s must be %s on %s, %d x %d, with contiguous rows" % (what, kind, device, m, width))
+        return t.data_ptr(), t.stride(0)
+
+    def vector(what, t):
+        if t is None:
+            return None
+        if t.dtype != dtype or t.device != device or t.shape != (width,) or (t.stride(0) != 1 and width > 1):
+            raise ValueError("%s must be a contiguous %s vector of %d on %s" % (what, dtype, width, device))
+        return t.data_ptr()
+
+    _need(weight_pre is not None, "weight_pre is needed")
+    xp, xs = rows("x", x, dtype)
+    rp, rs = rows("residual", residual, residual.dtype)
+    yp, ys = rows("residual_out", residual_out, residual.dtype)
+    op, os = rows("out", out, dtype)
+    if gate is not None and gate.dim() == 1:
+        gp, gs = vector("gate", gate), 0
+    else:
+        gp, gs = rows("gate", gate, dtype)
+    args = _Norm(xp, rp, gp, vector("weight_post", weight_post), vector("weight_pre", weight_pre), yp, op,
+                 xs, rs, gs, ys, os, width, DTYPES[dtype], DTYPES[residual.dtype], alpha, eps)
+    _fail(_lib().blk_norm_run(args, m, _raw_stream(stream, device)), "norm_run")

@@ -30,6 +30,8 @@ SOURCES = [
     "wide_dma_variants.hip",
     "attn.hip",
     "attn_rows.hip",
+    "w4.hip",
+    "norm.hip",
 ]
 
 ARCH = os.environ.get("GDP_OFFLOAD_ARCH", "gfx950")

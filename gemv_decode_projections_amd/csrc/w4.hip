@@ -1,0 +1,337 @@
+// Products with 4-bit weights and group scales (include/block.h, blk_w4_*):
+//     out[m, n] = sum over groups g of s[n, g] * sum over k in g of (q[n, k] - z[n, g]) x[m, k].
+//
+// The weights become matrix operands without a conversion instruction: the
+// 16-bit pattern 0x4300 | q is the BF16 number 128 + q (0x6400 | q the FP16
+// number 1024 + q), so two weights take one shift and one and-or. Products are
+// exact, sums FP32, and the scale multiplies the group's FP32 sum, so no
+// weight is ever rounded. The offset comes off
+//   FP16: exactly, by one packed subtraction of 1024 + z before the product;
+//   BF16 (no packed subtraction): from the group's sum, as (128 + z) * sum x,
+//         with sum x from a product with ones, one per 32 k for all rows.
+// The sums then hold up to 136 |sum x| next to the result, which costs about
+// 2^-24 * 136 / 4.6 of it, far below the output's 2^-9.
+//
+// Memory bound at the token counts it is for (16 tokens: 64 operations per
+// weight byte). A workgroup owns RB blocks of 16 rows and 16 NT tokens; its
+// eight waves split K, each unit of 128 k is one 16-byte load per lane and row
+// block, 1 KB contiguous per wave.
+#include <limits.h>
+
+#include "block_common.h"
+
+namespace gdp {
+namespace {
+
+constexpr int kUnitK = 128;            // k per 16-byte load of a lane
+constexpr int kW4Waves = 8;
+
+struct W4Args {
+    const u32x4 *w;                    // [row block][unit][lane]
+    const char *scale;                 // [row block][unit][128 / G][16 rows], 16 bits
+    const char *zero;                  // same shape: 128 + z (1024 + z); nullptr: z = 8
+    const char *x;
+    char *out;
+    int64_t x_stride, out_stride;      // bytes
+    int n, k, m, units, blocks;
+    int wide_out;                      // output rows take 8-byte stores
+};
+
+// Weight pair j (elements 2j and 2j + 1 of the eight in w) with its offset.
+template <class T>
+__device__ __forceinline__ uint32_t weight_pair(uint32_t w, int j)
+{
+    constexpr uint32_t magic = T::kId == BLK_BF16 ? 0x43004300u : 0x64006400u;
+    return ((w >> (4 * j)) & 0x000f000fu) | magic;
+}
+
+template <class T, int G, int RB, int NT>
+__global__ __launch_bounds__(64 * kW4Waves) void w4_kernel(W4Args a)
+{
+    constexpr bool BF = T::kId == BLK_BF16;
+    constexpr int GPU_ = kUnitK / G;   // groups per unit
+    constexpr int SPG = G / 32;        // k-steps per group
+    __shared__ f32x4 s_part[kW4Waves][RB * NT][kWave];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int col = lane % 16, quad = lane / 16;
+    const int rb0 = blockIdx.x * RB;
+    const int tok0 = blockIdx.y * 16 * NT;
+    const int u0 = (int)((int64_t)wave * a.units / kW4Waves), u1 = (int)((int64_t)(wave + 1) * a.units / kW4Waves);
+
+    const char *xp[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        xp[t] = a.x + (int64_t)min(tok0 + 16 * t + col, a.m - 1) * a.x_stride + quad * 16;
+
+    f32x4 acc[RB][NT];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint32_t one = BF ? 0x3f803f80u : 0x3c003c00u;
+    const u32x4 ones = {one, one, one, one};
+
+    for (int u = u0; u < u1; ++u) {
+        u32x4 w[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+            w[r] = a.w[((int64_t)min(rb0 + r, a.blocks - 1) * a.units + u) * kWave + lane];
+        u32x4 xf[NT][4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            if (u * kUnitK + 32 * s < a.k)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    xf[t][s] = *reinterpret_cast<const u32x4 *>(xp[t] + ((int64_t)u * kUnitK + 32 * s) * 2);
+#pragma unroll
+        for (int g = 0; g < GPU_; ++g) {
+            if (u * kUnitK + G * g >= a.k)
+                break;
+            f32x4 xs[NT];
+            if constexpr (BF)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    xs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < SPG; ++s)
+                        xs[t] = T::mfma16(ones, xf[t][g * SPG + s], xs[t]);
+                }
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const int64_t group = (((int64_t)min(rb0 + r, a.blocks - 1) * a.units + u) * GPU_ + g) * 32;
+                const u32x2 sc = *reinterpret_cast<const u32x2 *>(a.scale + group + quad * 8);
+                u32x2 zc = {BF ? 0x43084308u : 0u, BF ? 0x43084308u : 0u};
+                uint32_t zrow = 0x64086408u;
+                if (a.zero) {
+                    if constexpr (BF)
+                        zc = *reinterpret_cast<const u32x2 *>(a.zero + group + quad * 8);
+                    else
+                        zrow = *reinterpret_cast<const uint16_t *>(a.zero + group + col * 2) * 0x10001u;
+                }
+                f32x4 part[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    part[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < SPG; ++s) {
+                    u32x4 wf;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t p = weight_pair<T>(w[r][g * SPG + s], j);
+                        if constexpr (!BF)
+                            p = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) - __builtin_bit_cast(f16x2, zrow));
+                        wf[j] = p;
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        part[t] = T::mfma16(wf, xf[t][g * SPG + s], part[t]);
+                }
+                const float sf[4] = {T::lo(sc.x), T::hi(sc.x), T::lo(sc.y), T::hi(sc.y)};
+                const float zf[4] = {T::lo(zc.x), T::hi(zc.x), T::lo(zc.y), T::hi(zc.y)};
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = part[t][i];
+                        if constexpr (BF)
+                            v -= zf[i] * xs[t][i];
+                        acc[r][t][i] += sf[i] * v;
+                    }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            s_part[wave][r * NT + t][lane] = acc[r][t];
+    __syncthreads();
+    for (int i = wave; i < RB * NT; i += kW4Waves) {
+        const int r = i / NT, t = i % NT;
+        f32x4 v = s_part[0][i][lane];
+#pragma unroll
+        for (int w = 1; w < kW4Waves; ++w)
+            v += s_part[w][i][lane];
+        const int tok = tok0 + 16 * t + col;
+        const int row = (rb0 + r) * 16 + 4 * quad;
+        if (tok >= a.m || row >= a.n)
+            continue;
+        char *o = a.out + (int64_t)tok * a.out_stride + (int64_t)row * 2;
+        const u32x2 p = {T::pack(v.x, v.y), T::pack(v.z, v.w)};
+        if (a.wide_out) {
+            *reinterpret_cast<u32x2 *>(o) = p;
+        } else {
+            const uint16_t h[4] = {(uint16_t)p.x, (uint16_t)(p.x >> 16), (uint16_t)p.y, (uint16_t)(p.y >> 16)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (row + e < a.n)
+                    reinterpret_cast<uint16_t *>(o)[e] = h[e];
+        }
+    }
+}
+
+// Packing: the operand order of the weights. Dword s of lane l's 16 bytes
+// holds the eight weights of row l % 16, k = 128 unit + 32 s + 8 (l / 16) +
+// 0..7, element 2j at bit 4j and 2j + 1 at bit 16 + 4j. Rows past n and k past
+// the matrix are zero.
+__global__ void w4_pack_kernel(const uint8_t *q, int64_t row_bytes, u32x4 *dst, int n, int k, int units, int64_t total)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= total)
+        return;
+    const int lane = (int)(id % kWave);
+    const int u = (int)(id / kWave % units);
+    const int row = (int)(id / kWave / units) * 16 + lane % 16;
+    u32x4 v;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int k0 = u * kUnitK + 32 * s + 8 * (lane / 16);
+        uint32_t w = 0;
+        if (row < n && k0 < k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t b = q[row * row_bytes + k0 / 2 + j];
+                w |= (b & 15u) << (4 * j) | (b >> 4) << (16 + 4 * j);
+            }
+        v[s] = w;
+    }
+    dst[id] = v;
+}
+
+template <class T>
+__global__ void w4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zeros, uint16_t *dscale, uint16_t *dzero,
+                                      int n, int groups, int padded, int64_t total)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= total)
+        return;
+    const int g = (int)(id / 16 % padded);
+    const int row = (int)(id / 16 / padded) * 16 + (int)(id % 16);
+    const bool in = row < n && g < groups;
+    dscale[id] = in ? scales[(int64_t)row * groups + g] : 0;
+    if (zeros) {
+        // 128 + z in BF16, 1024 + z in FP16: z of one byte, 0..15.
+        const uint32_t z = in ? zeros[(int64_t)row * groups + g] & 15u : 8u;
+        dzero[id] = (uint16_t)((T::kId == BLK_BF16 ? 0x4300u : 0x6400u) | z);
+    }
+}
+
+using W4Kernel = void (*)(W4Args);
+
+template <class T, int G>
+W4Kernel pick(int nt)
+{
+    return nt == 1 ? w4_kernel<T, G, 1, 1> : nt == 2 ? w4_kernel<T, G, 2, 2> : w4_kernel<T, G, 2, 4>;
+}
+
+template <class T>
+W4Kernel pick(int group, int nt)
+{
+    return group == 32 ? pick<T, 32>(nt) : group == 64 ? pick<T, 64>(nt) : pick<T, 128>(nt);
+}
+
+struct Layout {
+    int units, blocks, padded;
+    size_t w, scale;                   // bytes of the weights, of the scales (and of the zeros)
+};
+
+bool layout(const blk_w4 *w, Layout &l)
+{
+    if (w->n < 1 || w->k < 1 || w->n > (1 << 24) || w->k > (1 << 24) || (w->group != 32 && w->group != 64 && w->group != 128) ||
+        w->k % w->group || (w->dtype != BLK_BF16 && w->dtype != BLK_F16))
+        return false;
+    l.units = (w->k + kUnitK - 1) / kUnitK;
+    l.blocks = (w->n + 15) / 16;
+    l.padded = l.units * (kUnitK / w->group);
+    l.w = (size_t)l.blocks * l.units * 1024;
+    l.scale = (size_t)l.blocks * l.padded * 32;
+    return true;
+}
+
+}  // namespace
+}  // namespace gdp
+
+using namespace gdp;
+
+extern "C" {
+
+size_t blk_w4_packed_bytes(const blk_w4 *w)
+{
+    Layout l;
+    return w && layout(w, l) ? l.w + l.scale * (w->has_zeros ? 2 : 1) : 0;
+}
+
+int blk_w4_pack(const blk_w4 *w, const void *q, const void *scales, const void *zeros, void *packed, void *stream)
+{
+    Layout l;
+    if (!w)
+        return PROJ_ERR_NULL;
+    if (!layout(w, l))
+        return PROJ_ERR_ARG;
+    if (!q || !scales || !packed || !zeros != !w->has_zeros)
+        return PROJ_ERR_NULL;
+    if (!aligned_to(packed, 16) || !aligned_to(scales, 2))
+        return PROJ_ERR_ALIGN;
+    const int64_t wt = (int64_t)l.blocks * l.units * kWave, st = (int64_t)l.blocks * l.padded * 16;
+    if (wt / 256 >= INT_MAX || st / 256 >= INT_MAX)
+        return PROJ_ERR_ARG;
+    char *p = static_cast<char *>(packed);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)((wt + 255) / 256)), dim3(256), 0, s,
+                       static_cast<const uint8_t *>(q), (int64_t)w->k / 2, reinterpret_cast<u32x4 *>(p), w->n, w->k,
+                       l.units, wt);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return hip_fail(e);
+    auto *kernel = w->dtype == BLK_BF16 ? w4_pack_scales_kernel<BF16> : w4_pack_scales_kernel<F16>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((st + 255) / 256)), dim3(256), 0, s,
+                       static_cast<const uint16_t *>(scales), static_cast<const uint8_t *>(zeros),
+                       reinterpret_cast<uint16_t *>(p + l.w), reinterpret_cast<uint16_t *>(p + l.w + l.scale), w->n,
+                       w->k / w->group, l.padded, st);
+    e = hipGetLastError();
+    return e == hipSuccess ? PROJ_OK : hip_fail(e);
+}
+
+int blk_w4_run(const blk_w4 *w, const void *packed, const void *x, int64_t x_stride, int m, void *out,
+               int64_t out_stride, void *stream)
+{
+    Layout l;
+    if (!w)
+        return PROJ_ERR_NULL;
+    if (!layout(w, l) || m < 0 || m > (1 << 20) || x_stride < 0 || x_stride % 8 || out_stride < 0 ||
+        x_stride >= ((int64_t)1 << 40) || out_stride >= ((int64_t)1 << 40))
+        return PROJ_ERR_ARG;
+    if (m == 0)
+        return PROJ_OK;
+    if (!packed || !x || !out)
+        return PROJ_ERR_NULL;
+    if (!aligned_to(packed, 16) || !aligned_to(x, 16) || !aligned_to(out, 2))
+        return PROJ_ERR_ALIGN;
+    const char *p = static_cast<const char *>(packed);
+    W4Args a{};
+    a.w = reinterpret_cast<const u32x4 *>(p);
+    a.scale = p + l.w;
+    a.zero = w->has_zeros ? p + l.w + l.scale : nullptr;
+    a.x = static_cast<const char *>(x);
+    a.out = static_cast<char *>(out);
+    a.x_stride = x_stride * 2;
+    a.out_stride = out_stride * 2;
+    a.n = w->n;
+    a.k = w->k;
+    a.m = m;
+    a.units = l.units;
+    a.blocks = l.blocks;
+    a.wide_out = w->n % 4 == 0 && out_stride % 4 == 0 && aligned_to(out, 8);
+    const int nt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+    const int rb = nt == 1 ? 1 : 2;
+    W4Kernel fn = w->dtype == BLK_BF16 ? pick<BF16>(w->group, nt) : pick<F16>(w->group, nt);
+    void *params[1] = {&a};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(fn),
+                                         dim3((l.blocks + rb - 1) / rb, (m + 16 * nt - 1) / (16 * nt)),
+                                         dim3(64 * kW4Waves), params, 0, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? PROJ_OK : hip_fail(e);
+}
+
+}  // extern "C"

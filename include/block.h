@@ -127,6 +127,55 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
                  void *stream);
 size_t blk_attn_workspace_bytes(int head_dim);
 
+/*
+ * Projections with 4-bit weights:
+ *     out[i, n] = sum over groups g of s[n, g] * sum over k in g of (q[n, k] - z[n, g]) * x[i, k]
+ * with n x k weights in groups of `group` consecutive k (32, 64 or 128; k a
+ * multiple of it). q: n x k / 2 bytes, element 2j in the low nibble of byte j.
+ * scales: n x k / group of dtype (BLK_BF16 or BLK_F16, the type of x and out
+ * too). zeros: n x k / group bytes of 0..15, or none (has_zeros 0): z = 8.
+ * n and k up to 2^24.
+ *
+ * blk_w4_pack lays them out once in `packed` (blk_w4_packed_bytes bytes,
+ * 16-byte aligned, of the caller); the sources may be freed when the stream
+ * has passed it. blk_w4_run: x is m x k, rows x_stride elements apart (a
+ * multiple of 8), 16-byte aligned; out m x n, rows out_stride apart. Made for
+ * small m (a decode step's tokens); any m up to 2^20 is right. One launch
+ * (none at m = 0).
+ */
+typedef struct {
+    int n, k, group, dtype, has_zeros;
+} blk_w4;
+
+size_t blk_w4_packed_bytes(const blk_w4 *w);     /* 0: not a shape of the operator */
+int blk_w4_pack(const blk_w4 *w, const void *q, const void *scales, const void *zeros, void *packed, void *stream);
+int blk_w4_run(const blk_w4 *w, const void *packed, const void *x, int64_t x_stride, int m, void *out,
+               int64_t out_stride, void *stream);
+
+/*
+ * blk_norm_run - the norms around a block, for m rows of `width` elements (1
+ * to 32768):
+ *     t = x * rsqrt(mean(x^2) + eps) * weight_post      (t = x without weight_post)
+ *     residual_out = residual + alpha * gate * t        (no gate: 1)
+ *     out = r * rsqrt(mean(r^2) + eps) * weight_pre     with r = residual_out before rounding
+ * x NULL (then no weight_post, gate and residual_out either): only the last
+ * line, of residual. x, gate, the weights and out are of dtype (BLK_BF16 or
+ * BLK_F16), residual and residual_out of residual_dtype (dtype or BLK_F32).
+ * residual_out may be residual, and out may be x. Row strides in elements; a
+ * gate_stride of 0 shares one gate row. Rows whose strides, pointers and
+ * width are multiples of 8 elements (16 bytes) are read 16 bytes at a time,
+ * others element by element. One launch (none at m = 0).
+ */
+typedef struct {
+    const void *x, *residual, *gate, *weight_post, *weight_pre;
+    void *residual_out, *out;
+    int64_t x_stride, residual_stride, gate_stride, residual_out_stride, out_stride;
+    int width, dtype, residual_dtype;
+    float alpha, eps;
+} blk_norm_args;
+
+int blk_norm_run(const blk_norm_args *args, int m, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
