@@ -107,7 +107,7 @@ class KvCache:
               "k and v differ in shape, strides, dtype or device")
         pages, size, heads, dim = k.shape
         _need(dim in HEAD_DIMS, "head_dim %d, expected one of %s" % (dim, HEAD_DIMS))
-        _need(size >= 4 and size & (size - 1) == 0, "page_size %d, expected a power of two, at least 4" % size)
+        _need(size >= 8 and size & (size - 1) == 0, "page_size %d, expected a power of two, at least 8" % size)
         self.k, self.v = k, v
         self.n_pages, self.page_size, self.kv_heads, self.head_dim = pages, size, heads, dim
         self.dtype, self.device = k.dtype, k.device

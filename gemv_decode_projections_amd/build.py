@@ -30,6 +30,7 @@ SOURCES = [
     "wide_dma_variants.hip",
     "attn.hip",
     "attn_rows.hip",
+    "attn_tile.hip",
     "w4.hip",
     "norm.hip",
 ]

@@ -42,7 +42,7 @@ struct AttnArgs {
 // is less than 2 r / C, and the ranges sum to at most target * C), so the
 // kernels aim at units in inverse proportion to their tile's rows and one
 // workspace serves all of them.
-constexpr int kAttnSlotRows = 65536;               // rows of all slots together
+constexpr int kAttnSlotRows = 131072;              // rows of all slots together
 constexpr int kAttnMaxTarget = 512;
 __host__ __device__ constexpr int attn_target(int rows)
 {
@@ -88,70 +88,95 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, 
 // positions, so a batch of any mix of lengths gives about `target` equal
 // units, or one per tile where there are many tiles. Every workgroup computes
 // the same partition from the device's lengths and finds its own unit.
+// Workgroups are dealt to the 8 XCDs round-robin; the units, ordered so that
+// the row tiles that read the same keys follow each other, are given to the
+// XCDs in contiguous eighths, so those tiles share an L2.
 // Returns false for workgroups past the last unit.
 template <int ROWS>
 __device__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
 {
     const int lane = threadIdx.x % kWave;
-    const int kvh = id % a.kv_heads;
-    const int want = id / a.kv_heads;
-    auto shape = [&](int b, int &tok0, int &n, int &len, int &tiles, int &first) {
-        tok0 = n = len = tiles = first = 0;
-        if (b < a.seqs) {
-            seq_bounds(a, b, tok0, n, len);
-            tiles = (n * a.group + ROWS - 1) / ROWS;
-            if (a.window > 0)
-                first = max(0, len - n - a.window + 1) / a.kv_step * a.kv_step;
-        }
-        return len - first;
+    struct Shape {
+        int tok0, n, len, tiles, first, range;
     };
-    int tok0, n, len, tiles, first;
-    int range = 0;
+    auto shape = [&](int b) {
+        Shape s = {0, 0, 0, 0, 0, 0};
+        if (b < a.seqs) {
+            seq_bounds(a, b, s.tok0, s.n, s.len);
+            s.tiles = (s.n * a.group + ROWS - 1) / ROWS;
+            if (a.window > 0)
+                s.first = max(0, s.len - s.n - a.window + 1) / a.kv_step * a.kv_step;
+            s.range = s.len - s.first;
+        }
+        return s;
+    };
+    Shape s;
     unsigned long long w = 0;
     for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
-        range = shape(b0 + lane, tok0, n, len, tiles, first);
-        w += (unsigned long long)tiles * (unsigned)range;
+        s = shape(b0 + lane);
+        w += (unsigned long long)s.tiles * (unsigned)s.range;
     }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2)
         w += __shfl_xor(w, d);
     w *= (unsigned)a.kv_heads;
     const unsigned long long per = (w + a.target - 1) / a.target;
-    const int c = (int)min((unsigned long long)0x40000000,
-                           max((unsigned long long)a.min_split, (per + a.kv_step - 1) / a.kv_step * a.kv_step));
+    // (read from the first lane, so that what follows stays in scalar registers)
+    const int c = __builtin_amdgcn_readfirstlane(
+        (int)min((unsigned long long)0x40000000,
+                 max((unsigned long long)a.min_split, (per + a.kv_step - 1) / a.kv_step * a.kv_step)));
+    auto units_of = [&](const Shape &x, int &splits) {
+        splits = max(1, (x.range + c - 1) / c);
+        return x.tiles * splits * a.kv_heads;
+    };
+    int splits;
+    int total = 0;
+    for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
+        if (a.seqs > kWave)
+            s = shape(b0 + lane);
+        total += units_of(s, splits);
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2)
+        total += __shfl_xor(total, d);
+    total = __builtin_amdgcn_readfirstlane(total);
+    const int per_xcd = (total + 7) / 8;
+    const int want = id % 8 * per_xcd + id / 8;
+    if (id / 8 >= per_xcd || want >= total)
+        return false;
     int units_before = 0, slots_before = 0;
     for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
         if (a.seqs > kWave)
-            range = shape(b0 + lane, tok0, n, len, tiles, first);
-        const int splits = max(1, (range + c - 1) / c);
-        const int units = tiles * splits;
+            s = shape(b0 + lane);
+        const int units = units_of(s, splits);
         const int slots = splits > 1 ? units : 0;
         const int usum = units_before + wave_scan(units, lane);
         const int ssum = slots_before + wave_scan(slots, lane);
         const unsigned long long mine = __ballot(usum > want);
         if (mine) {
             const int l = __ffsll(mine) - 1;
-            const int local = want - __shfl(usum - units, l);
+            auto of = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+            const int local = want - of(usum - units);
+            const int tiles = of(s.tiles);
             u.seq = b0 + l;
-            u.tok0 = __shfl(tok0, l);
-            u.n = __shfl(n, l);
-            u.len = __shfl(len, l);
-            u.splits = __shfl(splits, l);
-            const int lo0 = __shfl(first, l);
-            const int tile = local / u.splits;
-            u.split = local - tile * u.splits;
-            u.slot0 = (__shfl(ssum - slots, l) + tile * u.splits) * a.kv_heads + kvh;
-            u.kvh = kvh;
+            u.tok0 = of(s.tok0);
+            u.n = of(s.n);
+            u.len = of(s.len);
+            u.splits = of(splits);
+            const int tile = local % tiles;
+            u.split = local / tiles % u.splits;
+            u.kvh = local / tiles / u.splits;
+            u.slot0 = of(ssum - slots) + (u.kvh * tiles + tile) * u.splits;
             u.row0 = tile * ROWS;
             u.nrows = min(ROWS, u.n * a.group - u.row0);
-            u.lo = lo0 + u.split * c;
+            u.lo = of(s.first) + u.split * c;
             // The tile's last token sees no further than its own position.
             const int last = u.len - u.n + (u.row0 + u.nrows - 1) / a.group;
             u.hi = min(u.split + 1 < u.splits ? u.lo + c : u.len, max(last + 1, 0));
             return true;
         }
-        units_before = __shfl(usum, kWave - 1);
-        slots_before = __shfl(ssum, kWave - 1);
+        units_before = __builtin_amdgcn_readlane(usum, kWave - 1);
+        slots_before = __builtin_amdgcn_readlane(ssum, kWave - 1);
     }
     return false;
 }
@@ -194,95 +219,115 @@ __device__ __forceinline__ void write_lse(const AttnArgs &a, const AttnUnit &u, 
             l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * 0.693147181f : -INFINITY;
 }
 
-// The workgroup's rows, unnormalised in LDS (o: rows x pitch floats, maxima m
-// in base-2 scaled scores, sums l), leave the unit: straight to the output if
-// the tile has one split. Otherwise they are published in the unit's slot
-// with stores that pass the XCD-local L2, the arrival is counted, and the
-// tile's last workgroup joins the splits in split order (so the result does
-// not depend on which came last).
-template <class T, int DIM, int ROWS, int THREADS>
-__device__ __forceinline__ void leave_unit(const AttnArgs &a, const AttnUnit &u, const float *o, int pitch,
-                                           const float *m, const float *l, int *flag)
+// The workgroup's rows, unnormalised, leave the unit: straight to the output
+// if the tile has one split. Otherwise they are published in the unit's slot
+// with stores that pass the XCD-local L2 and the arrival is counted; the last
+// of every kJoin consecutive splits joins those, and where there are more
+// splits the joins are joined the same way, each result in the slot of its
+// first split. A join thus reads at most kJoin slots, all loads in flight, and
+// always in split order: the result does not depend on who came last.
+// Measured: one workgroup joining all splits took 290 us of a 340 us call (16
+// tiles of 64 rows in 30 splits each); the joins of kJoin take about 2 us a
+// level.
+// pieces(f) calls f(row, d, value, m, l) for the four elements d.. of each of
+// the calling thread's pieces, m and l the row's maximum (in base-2 scaled
+// scores) and sum.
+constexpr int kJoin = 16;
+
+template <class T, int DIM, int ROWS, int THREADS, class Pieces>
+__device__ __forceinline__ void leave_unit(const AttnArgs &a, const AttnUnit &u, Pieces pieces, int *flag)
 {
     const int tid = threadIdx.x;
-    constexpr int PER = DIM / 4;               // threads per row
-    constexpr int STEP = THREADS / PER;        // rows per pass
-    const int d = 4 * (tid % PER);
     if (u.splits == 1) {
-        for (int r = tid / PER; r < u.nrows; r += STEP) {
-            const float sum = l[r];
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(o + r * pitch + d);
-            write_out<T>(a, u, u.row0 + r, d, v, sum == 0.f ? 0.f : 1.0f / sum);
+        pieces([&](int r, int d, f32x4 v, float m, float l) {
+            write_out<T>(a, u, u.row0 + r, d, v, l == 0.f ? 0.f : 1.0f / l);
             if (d == 0)
-                write_lse(a, u, u.row0 + r, m[r], sum);
-        }
+                write_lse(a, u, u.row0 + r, m, l);
+        });
         return;
     }
     constexpr uint32_t SLOT = ROWS * (DIM + 2) * 4u;
     constexpr uint32_t stats = ROWS * DIM * 4u;
     const __amdgpu_buffer_rsrc_t ws =
         __builtin_amdgcn_make_buffer_rsrc(a.slots, 0, (int)(kAttnSlotRows * (DIM + 2) * 4u), 0x00020000);
-    // Consecutive slots of a tile are kv_heads apart.
-    auto slot = [&](int s) { return (uint32_t)(u.slot0 + s * a.kv_heads) * SLOT; };
-    const uint32_t mine = slot(u.split);
-    for (int r = tid / PER; r < u.nrows; r += STEP) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(o + r * pitch + d);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ws, mine + (uint32_t)(r * DIM + d) * 4u, 0,
+    auto publish = [&](int split, int r, int d, f32x4 v, float m, float l) {
+        const uint32_t at = (uint32_t)(u.slot0 + split) * SLOT;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ws, at + (uint32_t)(r * DIM + d) * 4u, 0,
                                                kDeviceScope);
         if (d == 0)
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__builtin_bit_cast(uint32_t, m[r]),
-                                                        __builtin_bit_cast(uint32_t, l[r])},
-                                                  ws, mine + stats + (uint32_t)r * 8u, 0, kDeviceScope);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (tid == 0) {
-        uint32_t *c = a.counters + u.slot0;
-        const uint32_t before = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const bool last = before == (uint32_t)(u.splits - 1);
-        if (last)
-            __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        *flag = last;
-    }
-    __syncthreads();
-    if (!*flag)
-        return;
-    for (int r = tid / PER; r < u.nrows; r += STEP) {
-        float top = -INFINITY, sum = 0.f;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        constexpr int CH = 4;                  // splits in flight
-        for (int s0 = 0; s0 < u.splits; s0 += CH) {
-            u32x2 st[CH];
-            u32x4 v[CH];
+            __builtin_amdgcn_raw_buffer_store_b64(
+                u32x2{__builtin_bit_cast(uint32_t, m), __builtin_bit_cast(uint32_t, l)}, ws,
+                at + stats + (uint32_t)r * 8u, 0, kDeviceScope);
+    };
+    pieces([&](int r, int d, f32x4 v, float m, float l) { publish(u.split, r, d, v, m, l); });
+    constexpr int PER = DIM / 4;               // threads per row
+    const int d = 4 * (tid % PER);
+    for (int stride = 1, level = 0;; stride *= kJoin, ++level) {
+        const int first = u.split / (stride * kJoin) * (stride * kJoin);
+        const int members = min(kJoin, (u.splits - first + stride - 1) / stride);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (tid == 0) {
+            // Counters of the levels lie at slots of different remainders.
+            uint32_t *c = a.counters + u.slot0 + first + level;
+            const uint32_t before = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const bool last = before == (uint32_t)(members - 1);
+            if (last)
+                __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            *flag = last;
+        }
+        __syncthreads();
+        if (!*flag)
+            return;
+        const bool done = first == 0 && stride * kJoin >= u.splits;
+        for (int r = tid / PER; r < u.nrows; r += THREADS / PER) {
+            u32x2 st[kJoin];
+            u32x4 v[kJoin];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const uint32_t at = slot(min(s0 + i, u.splits - 1));
-                st[i] = __builtin_amdgcn_raw_buffer_load_b64(ws, at + stats + (uint32_t)r * 8u, 0, kDeviceScope);
-                v[i] = __builtin_amdgcn_raw_buffer_load_b128(ws, at + (uint32_t)(r * DIM + d) * 4u, 0, kDeviceScope);
-            }
+            for (int i = 0; i < kJoin; ++i)
+                if (i < members) {
+                    const uint32_t at = (uint32_t)(u.slot0 + first + i * stride) * SLOT;
+                    st[i] = __builtin_amdgcn_raw_buffer_load_b64(ws, at + stats + (uint32_t)r * 8u, 0, kDeviceScope);
+                    v[i] = __builtin_amdgcn_raw_buffer_load_b128(ws, at + (uint32_t)(r * DIM + d) * 4u, 0, kDeviceScope);
+                }
+            float top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                if (s0 + i >= u.splits)
-                    break;
-                // (by value: a bit cast of a vector's element takes element 0)
-                const uint32_t mbits = st[i].x, lbits = st[i].y;
-                const float ms = __builtin_bit_cast(float, mbits);
-                const float big = fmaxf(top, ms);
-                const float safe = big == -INFINITY ? 0.f : big;
-                const float f = exp2_fast(top - safe), g = exp2_fast(ms - safe);
-                acc = acc * f + __builtin_bit_cast(f32x4, v[i]) * g;
-                sum = sum * f + __builtin_bit_cast(float, lbits) * g;
-                top = big;
+            for (int i = 0; i < kJoin; ++i)
+                if (i < members) {
+                    // (by value: a bit cast of a vector's element takes element 0)
+                    const uint32_t bits = st[i].x;
+                    top = fmaxf(top, __builtin_bit_cast(float, bits));
+                }
+            const float safe = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i)
+                if (i < members) {
+                    const uint32_t mbits = st[i].x, lbits = st[i].y;
+                    const float f = exp2_fast(__builtin_bit_cast(float, mbits) - safe);
+                    sum += f * __builtin_bit_cast(float, lbits);
+                    acc += f * __builtin_bit_cast(f32x4, v[i]);
+                }
+            if (done) {
+                write_out<T>(a, u, u.row0 + r, d, acc, sum == 0.f ? 0.f : 1.0f / sum);
+                if (d == 0)
+                    write_lse(a, u, u.row0 + r, top, sum);
+            } else {
+                publish(first, r, d, acc, top, sum);
             }
         }
-        write_out<T>(a, u, u.row0 + r, d, acc, sum == 0.f ? 0.f : 1.0f / sum);
-        if (d == 0)
-            write_lse(a, u, u.row0 + r, top, sum);
+        if (done)
+            return;
     }
 }
 
+constexpr int kTilePos = 64;               // positions of the tile kernel's tiles
+
 using AttnKernel = void (*)(AttnArgs);
-// Row kernels for tiles of 16 * nb rows (nb 1, 2, 4); nullptr if not built.
+// Row kernels for tiles of 16 * nb rows (nb 1, 2); nullptr if not built.
 AttnKernel attn_rows_kernel(int dtype, int dim, int nb);
+// Tile kernels for tiles of 32 * waves rows (waves 2, 4), 64 * waves threads.
+AttnKernel attn_tile_kernel(int dtype, int dim, int waves);
 
 }  // namespace gdp

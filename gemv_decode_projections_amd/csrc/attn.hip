@@ -94,7 +94,7 @@ int check_cache(const blk_cache *c)
         return PROJ_ERR_ARG;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
         return PROJ_ERR_ARG;
-    if (c->n_pages < 1 || c->kv_heads < 1 || c->kv_heads > 65535 || c->page_size < 4 ||
+    if (c->n_pages < 1 || c->kv_heads < 1 || c->kv_heads > 65535 || c->page_size < 8 ||
         (c->page_size & (c->page_size - 1)))
         return PROJ_ERR_ARG;
     if (!stride_ok(c->page_stride) || !stride_ok(c->token_stride) || !stride_ok(c->head_stride) ||
@@ -287,19 +287,34 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
     a.slots = static_cast<char *>(ws) + kAttnCounterBytes;
 
     const int64_t seq_rows = (int64_t)std::min(args->max_q, batch->tokens) * a.group;
-    const int nb = seq_rows <= 16 ? 1 : seq_rows <= 32 || cache->head_dim == 256 ? 2 : 4;
-    const int tile = 16 * nb;
-    const void *fn = reinterpret_cast<const void *>(attn_rows_kernel(cache->dtype, cache->head_dim, nb));
-    a.kv_step = 128;
-    a.min_split = 128;
+    // Up to 32 rows per sequence and key head take the row kernel, which holds
+    // keys and values in registers; more take the tile kernel.
+    const void *fn;
+    int tile, threads;
+    if (seq_rows <= 32) {
+        const int nb = seq_rows <= 16 ? 1 : 2;
+        tile = 16 * nb;
+        threads = 256;
+        a.kv_step = 128;
+        a.min_split = 128;
+        fn = reinterpret_cast<const void *>(attn_rows_kernel(cache->dtype, cache->head_dim, nb));
+    } else {
+        const int waves = seq_rows <= 64 ? 2 : 4;
+        tile = 32 * waves;
+        threads = 64 * waves;
+        a.kv_step = kTilePos;
+        a.min_split = 4 * kTilePos;
+        fn = reinterpret_cast<const void *>(attn_tile_kernel(cache->dtype, cache->head_dim, waves));
+    }
     a.target = attn_target(tile);
     // Units: one per row tile and key head, and at most `target` more.
     const int64_t tiles = (rows / tile + batch->seqs) * a.kv_heads;
     const int64_t positions = (int64_t)batch->table_width * cache->page_size;
-    const int64_t grid = std::min(tiles + a.target, tiles * ((positions + a.min_split - 1) / a.min_split));
+    const int64_t grid =
+        (std::min(tiles + a.target, tiles * ((positions + a.min_split - 1) / a.min_split)) + 7) / 8 * 8;
     if (grid > 0x7fffffff)
         return PROJ_ERR_ARG;
-    return launch(fn, dim3((unsigned)grid), dim3(256), &a, stream);
+    return launch(fn, dim3((unsigned)grid), dim3(threads), &a, stream);
 }
 
 }  // extern "C"

@@ -1,4 +1,4 @@
-// Attention of few rows (up to 64 per tile: single tokens and drafted tokens)
+// Attention of few rows (up to 32 per tile: single tokens, a few drafted ones)
 // over a paged cache. Memory bound: every key and value is read once, as long
 // as a sequence's rows fit one tile, and straight into registers.
 //
@@ -175,6 +175,7 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
         for (int t = 0; t < 2; ++t)
             ok[t] = (unsigned)pg.v[t] < (unsigned)a.n_pages;
         const bool masked = base < all_lo || base + STEP > all_hi || base + STEP > u.hi || !__all(ok[0] && ok[1]);
+        bool poisoned = false;
         if (masked) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -193,6 +194,25 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
                         for (int e = 0; e < VEC / 2; ++e)
                             vr[h][4 * t + i][e] = held ? vr[h][4 * t + i][e] : 0u;
                 }
+            // A value that only some rows see may be an infinity or a NaN, which
+            // a zero weight does not silence in a product: it is left out of
+            // the product and added to the rows that see it.
+#pragma unroll
+            for (int h = 0; h < HALF; ++h)
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+#pragma unroll
+                    for (int e = 0; e < VEC / 2; ++e)
+                        poisoned |= not_finite<T>(vr[h][p][e]);
+            poisoned = __any(poisoned);
+            if (poisoned)
+#pragma unroll
+                for (int h = 0; h < HALF; ++h)
+#pragma unroll
+                    for (int p = 0; p < 8; ++p)
+#pragma unroll
+                        for (int e = 0; e < VEC / 2; ++e)
+                            vr[h][p][e] = finite_only<T>(vr[h][p][e]);
         }
         u32x4 pf[NB];
 #pragma unroll
@@ -240,6 +260,34 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
                 for (int nb = 0; nb < NB; ++nb)
                     acc[nb][h][j] = T::mfma16(vt[j], pf[nb], acc[nb][h][j]);
         }
+        if (poisoned)
+            for (int pos = 0; pos < STEP; ++pos) {
+                int64_t off;
+                if (base + pos >= u.hi || !kv_offset(a, page_of(base + pos), base + pos, head_off, off))
+                    continue;
+                const char *p = a.v + off + VEC * 4 * quad * 2;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const int slot = pos / 16 * 4 + pos % 4;
+                    const uint32_t pair = slot < 2 ? pf[nb][0] : slot < 4 ? pf[nb][1] : slot < 6 ? pf[nb][2] : pf[nb][3];
+                    const float w = __shfl(slot % 2 ? T::hi(pair) : T::lo(pair), pos / 4 % 4 * 16 + col);
+                    if (base + pos < see_lo[nb] || base + pos >= see_hi[nb])
+                        continue;
+#pragma unroll
+                    for (int h = 0; h < HALF; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < VEC; j += 2) {
+                                const uint32_t x =
+                                    *reinterpret_cast<const uint32_t *>(p + (h * 16 * VEC + VEC * i + j) * 2);
+                                if (!__builtin_isfinite(T::lo(x)))
+                                    acc[nb][h][j][i] += w * T::lo(x);
+                                if (!__builtin_isfinite(T::hi(x)))
+                                    acc[nb][h][j + 1][i] += w * T::hi(x);
+                            }
+                }
+            }
         if (after < u.hi)
             load_v(after, next);
         pg = next;
@@ -309,7 +357,14 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
             s_l[0][nb * 16 + col] = wl[nb];
         }
     __syncthreads();
-    leave_unit<T, DIM, ROWS, 256>(a, u, s_o, PITCH, s_m[0], s_l[0], &s_flag);
+    leave_unit<T, DIM, ROWS, 256>(
+        a, u,
+        [&](auto f) {
+            const int d = 4 * (threadIdx.x % (DIM / 4));
+            for (int r = threadIdx.x / (DIM / 4); r < u.nrows; r += 256 / (DIM / 4))
+                f(r, d, *reinterpret_cast<const f32x4 *>(s_o + r * PITCH + d), s_m[0][r], s_l[0][r]);
+        },
+        &s_flag);
 }
 
 }  // namespace gdp

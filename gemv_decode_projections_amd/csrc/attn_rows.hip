@@ -6,16 +6,7 @@ namespace gdp {
 template <class T, int DIM>
 static AttnKernel pick(int nb)
 {
-    switch (nb) {
-    case 1: return attn_rows<T, DIM, 1>;
-    case 2: return attn_rows<T, DIM, 2>;
-    case 4:
-        // 64 rows of 256 elements would not fit the registers.
-        if constexpr (DIM < 256)
-            return attn_rows<T, DIM, 4>;
-        [[fallthrough]];
-    default: return nullptr;
-    }
+    return nb == 1 ? attn_rows<T, DIM, 1> : nb == 2 ? attn_rows<T, DIM, 2> : nullptr;
 }
 
 template <class T>

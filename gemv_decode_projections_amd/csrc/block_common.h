@@ -29,6 +29,7 @@ struct BF16 {
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
     static __device__ __forceinline__ float lo(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
     static __device__ __forceinline__ float hi(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
+    static constexpr uint32_t kExponent = 0x7f80u;
 };
 
 struct F16 {
@@ -50,7 +51,23 @@ struct F16 {
     }
     static __device__ __forceinline__ float lo(uint32_t u) { return (float)__builtin_bit_cast(f16x2, u).x; }
     static __device__ __forceinline__ float hi(uint32_t u) { return (float)__builtin_bit_cast(f16x2, u).y; }
+    static constexpr uint32_t kExponent = 0x7c00u;
 };
+
+// Whether either of two packed values is an infinity or a NaN.
+template <class T>
+__device__ __forceinline__ bool not_finite(uint32_t u)
+{
+    constexpr uint32_t e = T::kExponent;
+    return (u & e) == e || (u & (e << 16)) == (e << 16);
+}
+// Both values with those replaced by zero.
+template <class T>
+__device__ __forceinline__ uint32_t finite_only(uint32_t u)
+{
+    constexpr uint32_t e = T::kExponent;
+    return ((u & e) == e ? 0u : u & 0xffffu) | ((u & (e << 16)) == (e << 16) ? 0u : u & 0xffff0000u);
+}
 
 // x combined with the lane 16 / 32 away, in the vector unit (no LDS trip).
 __device__ __forceinline__ float other16(float x, float &same)

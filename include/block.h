@@ -35,7 +35,7 @@ enum blk_dtype { BLK_BF16 = 0, BLK_F16 = 1, BLK_F32 = 2 };
  *     page * page_stride + token * token_stride + head * head_stride + d
  * elements past its pointer, so token-major and head-major pages, and keys
  * and values interleaved in one tensor, are all described.
- *   page_size  a power of two, at least 4
+ *   page_size  a power of two, at least 8
  *   head_dim   64, 128 or 256
  *   dtype      BLK_BF16 or BLK_F16
  *   strides    multiples of 8 elements, non-negative; page_stride below 2^31,
