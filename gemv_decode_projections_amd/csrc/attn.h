@@ -61,16 +61,31 @@ struct AttnUnit {
     int split, splits, slot0;
 };
 
-__device__ __forceinline__ int wave_scan(int x, int lane)
+// Inclusive sums over the wave's lanes, in the vector unit: within rows of 16
+// lanes, then the rows' totals passed on (row_shr 1, 2, 4, 8, row_bcast 15, 31).
+template <int CTRL, int ROWMASK>
+__device__ __forceinline__ int lane_moved(int x)
 {
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const int y = __shfl_up(x, d);
-        if (lane >= d)
-            x += y;
-    }
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWMASK, 0xf, false);
+}
+template <int CTRL, int ROWMASK>
+__device__ __forceinline__ unsigned long long lane_moved(unsigned long long x)
+{
+    return (unsigned long long)(unsigned)lane_moved<CTRL, ROWMASK>((int)(x >> 32)) << 32 |
+           (unsigned)lane_moved<CTRL, ROWMASK>((int)x);
+}
+template <class I>
+__device__ __forceinline__ I wave_scan(I x)
+{
+    x += lane_moved<0x111, 0xf>(x);
+    x += lane_moved<0x112, 0xf>(x);
+    x += lane_moved<0x114, 0xf>(x);
+    x += lane_moved<0x118, 0xf>(x);
+    x += lane_moved<0x142, 0xa>(x);
+    x += lane_moved<0x143, 0xc>(x);
     return x;
 }
+__device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, kWave - 1); }
 
 // New tokens and cached positions of sequence b, bounded to the tensors.
 __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, int &n, int &len)
@@ -87,98 +102,120 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, 
 // every tile's range is cut in parts of C = max(min_split, W / target)
 // positions, so a batch of any mix of lengths gives about `target` equal
 // units, or one per tile where there are many tiles. Every workgroup computes
-// the same partition from the device's lengths and finds its own unit.
-// Workgroups are dealt to the 8 XCDs round-robin; the units, ordered so that
-// the row tiles that read the same keys follow each other, are given to the
-// XCDs in contiguous eighths, so those tiles share an L2.
-// Returns false for workgroups past the last unit.
+// the same partition from the device's lengths, one lane per sequence.
 template <int ROWS>
-__device__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
-{
-    const int lane = threadIdx.x % kWave;
+struct Partition {
     struct Shape {
         int tok0, n, len, tiles, first, range;
     };
-    auto shape = [&](int b) {
-        Shape s = {0, 0, 0, 0, 0, 0};
+    const AttnArgs &a;
+    Shape s;             // the lane's sequence of the last 64 looked at
+    int c;
+
+    __device__ Shape shape(int b) const
+    {
+        Shape x = {0, 0, 0, 0, 0, 0};
         if (b < a.seqs) {
-            seq_bounds(a, b, s.tok0, s.n, s.len);
-            s.tiles = (s.n * a.group + ROWS - 1) / ROWS;
+            seq_bounds(a, b, x.tok0, x.n, x.len);
+            x.tiles = (x.n * a.group + ROWS - 1) / ROWS;
             if (a.window > 0)
-                s.first = max(0, s.len - s.n - a.window + 1) / a.kv_step * a.kv_step;
-            s.range = s.len - s.first;
+                x.first = max(0, x.len - x.n - a.window + 1) / a.kv_step * a.kv_step;
+            x.range = x.len - x.first;
         }
-        return s;
-    };
-    Shape s;
-    unsigned long long w = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
-        s = shape(b0 + lane);
-        w += (unsigned long long)s.tiles * (unsigned)s.range;
+        return x;
     }
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2)
-        w += __shfl_xor(w, d);
-    w *= (unsigned)a.kv_heads;
-    const unsigned long long per = (w + a.target - 1) / a.target;
-    // (read from the first lane, so that what follows stays in scalar registers)
-    const int c = __builtin_amdgcn_readfirstlane(
-        (int)min((unsigned long long)0x40000000,
-                 max((unsigned long long)a.min_split, (per + a.kv_step - 1) / a.kv_step * a.kv_step)));
-    auto units_of = [&](const Shape &x, int &splits) {
-        splits = max(1, (x.range + c - 1) / c);
-        return x.tiles * splits * a.kv_heads;
-    };
-    int splits;
-    int total = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
-        if (a.seqs > kWave)
-            s = shape(b0 + lane);
-        total += units_of(s, splits);
+    __device__ explicit Partition(const AttnArgs &args) : a(args)
+    {
+        unsigned long long w = 0;
+        for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
+            s = shape(b0 + (int)(threadIdx.x % kWave));
+            w += (unsigned long long)s.tiles * (unsigned)s.range;
+        }
+        w = wave_scan(w);
+        w = ((unsigned long long)(unsigned)last_lane((int)(w >> 32)) << 32 | (unsigned)last_lane((int)w)) *
+            (unsigned)a.kv_heads;
+        const unsigned long long per = (w + a.target - 1) / a.target;
+        c = (int)min((unsigned long long)0x40000000,
+                     max((unsigned long long)a.min_split, (per + a.kv_step - 1) / a.kv_step * a.kv_step));
     }
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2)
-        total += __shfl_xor(total, d);
-    total = __builtin_amdgcn_readfirstlane(total);
+    __device__ int splits() const { return max(1, (s.range + c - 1) / c); }
+    __device__ int units() const { return s.tiles * splits() * a.kv_heads; }
+    __device__ int slots() const { return splits() > 1 ? units() : 0; }
+    // Rows whose splits have to be joined.
+    __device__ int joins() const { return splits() > 1 ? s.n * a.group * a.kv_heads : 0; }
+
+    template <class Count>
+    __device__ int total(Count count)
+    {
+        int t = 0;
+        for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
+            if (a.seqs > kWave)
+                s = shape(b0 + (int)(threadIdx.x % kWave));
+            t += count(*this);
+        }
+        return last_lane(wave_scan(t));
+    }
+    // Finds item `want` (below the total) of those that `count` gives per
+    // sequence: sets u's sequence and its first slot, returns the item's
+    // number inside the sequence.
+    template <class Count>
+    __device__ int find(int want, Count count, AttnUnit &u, int &tiles)
+    {
+        int items_before = 0, slots_before = 0;
+        for (int b0 = 0;; b0 += kWave) {
+            if (a.seqs > kWave)
+                s = shape(b0 + (int)(threadIdx.x % kWave));
+            const int isum = items_before + wave_scan(count(*this));
+            const int ssum = slots_before + wave_scan(slots());
+            const unsigned long long mine = __ballot(isum > want);
+            if (mine || b0 + kWave >= a.seqs) {
+                const int l = mine ? __ffsll(mine) - 1 : 0;
+                auto of = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+                u.seq = b0 + l;
+                u.tok0 = of(s.tok0);
+                u.n = of(s.n);
+                u.len = of(s.len);
+                u.splits = of(splits());
+                u.lo = of(s.first);
+                u.slot0 = of(ssum - slots());
+                tiles = of(s.tiles);
+                return want - of(isum - count(*this));
+            }
+            items_before = last_lane(isum);
+            slots_before = last_lane(ssum);
+        }
+    }
+};
+
+// The workgroup's unit; false for workgroups past the last one. Workgroups are
+// dealt to the 8 XCDs round-robin; the units are given to the XCDs in
+// contiguous eighths, ordered so that the row tiles that read the same keys
+// follow each other and share an L2, then the heads that lie next to each
+// other in a page (with the heads apart in time 32 sequences x 8 heads took
+// 145 us instead of 131).
+template <int ROWS>
+__device__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
+{
+    Partition<ROWS> part(a);
+    auto units = [](const Partition<ROWS> &p) { return p.units(); };
+    const int total = part.total(units);
     const int per_xcd = (total + 7) / 8;
     const int want = id % 8 * per_xcd + id / 8;
     if (id / 8 >= per_xcd || want >= total)
         return false;
-    int units_before = 0, slots_before = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
-        if (a.seqs > kWave)
-            s = shape(b0 + lane);
-        const int units = units_of(s, splits);
-        const int slots = splits > 1 ? units : 0;
-        const int usum = units_before + wave_scan(units, lane);
-        const int ssum = slots_before + wave_scan(slots, lane);
-        const unsigned long long mine = __ballot(usum > want);
-        if (mine) {
-            const int l = __ffsll(mine) - 1;
-            auto of = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
-            const int local = want - of(usum - units);
-            const int tiles = of(s.tiles);
-            u.seq = b0 + l;
-            u.tok0 = of(s.tok0);
-            u.n = of(s.n);
-            u.len = of(s.len);
-            u.splits = of(splits);
-            const int tile = local % tiles;
-            u.split = local / tiles % u.splits;
-            u.kvh = local / tiles / u.splits;
-            u.slot0 = of(ssum - slots) + (u.kvh * tiles + tile) * u.splits;
-            u.row0 = tile * ROWS;
-            u.nrows = min(ROWS, u.n * a.group - u.row0);
-            u.lo = of(s.first) + u.split * c;
-            // The tile's last token sees no further than its own position.
-            const int last = u.len - u.n + (u.row0 + u.nrows - 1) / a.group;
-            u.hi = min(u.split + 1 < u.splits ? u.lo + c : u.len, max(last + 1, 0));
-            return true;
-        }
-        units_before = __builtin_amdgcn_readlane(usum, kWave - 1);
-        slots_before = __builtin_amdgcn_readlane(ssum, kWave - 1);
-    }
-    return false;
+    int tiles;
+    const int local = part.find(want, units, u, tiles);
+    const int tile = local % tiles;
+    u.kvh = local / tiles % a.kv_heads;
+    u.split = local / tiles / a.kv_heads;
+    u.slot0 += (u.kvh * tiles + tile) * u.splits;
+    u.row0 = tile * ROWS;
+    u.nrows = min(ROWS, u.n * a.group - u.row0);
+    u.lo += u.split * part.c;
+    // The tile's last token sees no further than its own position.
+    const int last = u.len - u.n + (u.row0 + u.nrows - 1) / a.group;
+    u.hi = min(u.split + 1 < u.splits ? u.lo + part.c : u.len, max(last + 1, 0));
+    return true;
 }
 
 // Byte offset of position p's key (or value) of the unit's head, and whether
@@ -219,115 +256,76 @@ __device__ __forceinline__ void write_lse(const AttnArgs &a, const AttnUnit &u, 
             l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * 0.693147181f : -INFINITY;
 }
 
-// The workgroup's rows, unnormalised, leave the unit: straight to the output
-// if the tile has one split. Otherwise they are published in the unit's slot
-// with stores that pass the XCD-local L2 and the arrival is counted; the last
-// of every kJoin consecutive splits joins those, and where there are more
-// splits the joins are joined the same way, each result in the slot of its
-// first split. A join thus reads at most kJoin slots, all loads in flight, and
-// always in split order: the result does not depend on who came last.
-// Measured: one workgroup joining all splits took 290 us of a 340 us call (16
-// tiles of 64 rows in 30 splits each); the joins of kJoin take about 2 us a
-// level.
-// pieces(f) calls f(row, d, value, m, l) for the four elements d.. of each of
-// the calling thread's pieces, m and l the row's maximum (in base-2 scaled
-// scores) and sum.
-constexpr int kJoin = 16;
+// Slots of the workspace, accessed past the XCD-local L2: they are exchanged
+// between workgroups.
+template <int DIM, int ROWS>
+struct Slots {
+    static constexpr uint32_t kSlot = ROWS * (DIM + 2) * 4u;
+    static constexpr uint32_t kStats = ROWS * DIM * 4u;
+    static constexpr uint32_t kEnd = kAttnSlotRows * (DIM + 2) * 4u;
+    const __amdgpu_buffer_rsrc_t ws;
 
-template <class T, int DIM, int ROWS, int THREADS, class Pieces>
-__device__ __forceinline__ void leave_unit(const AttnArgs &a, const AttnUnit &u, Pieces pieces, int *flag)
-{
-    const int tid = threadIdx.x;
-    if (u.splits == 1) {
-        pieces([&](int r, int d, f32x4 v, float m, float l) {
-            write_out<T>(a, u, u.row0 + r, d, v, l == 0.f ? 0.f : 1.0f / l);
-            if (d == 0)
-                write_lse(a, u, u.row0 + r, m, l);
-        });
-        return;
+    __device__ explicit Slots(const AttnArgs &a)
+        : ws(__builtin_amdgcn_make_buffer_rsrc(a.slots, 0, (int)kEnd, 0x00020000))
+    {
     }
-    constexpr uint32_t SLOT = ROWS * (DIM + 2) * 4u;
-    constexpr uint32_t stats = ROWS * DIM * 4u;
-    const __amdgpu_buffer_rsrc_t ws =
-        __builtin_amdgcn_make_buffer_rsrc(a.slots, 0, (int)(kAttnSlotRows * (DIM + 2) * 4u), 0x00020000);
-    auto publish = [&](int split, int r, int d, f32x4 v, float m, float l) {
-        const uint32_t at = (uint32_t)(u.slot0 + split) * SLOT;
+    __device__ __forceinline__ void put(int slot, int r, int d, f32x4 v, float m, float l) const
+    {
+        const uint32_t at = (uint32_t)slot * kSlot;
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ws, at + (uint32_t)(r * DIM + d) * 4u, 0,
                                                kDeviceScope);
         if (d == 0)
             __builtin_amdgcn_raw_buffer_store_b64(
                 u32x2{__builtin_bit_cast(uint32_t, m), __builtin_bit_cast(uint32_t, l)}, ws,
-                at + stats + (uint32_t)r * 8u, 0, kDeviceScope);
-    };
-    pieces([&](int r, int d, f32x4 v, float m, float l) { publish(u.split, r, d, v, m, l); });
-    constexpr int PER = DIM / 4;               // threads per row
-    const int d = 4 * (tid % PER);
-    for (int stride = 1, level = 0;; stride *= kJoin, ++level) {
-        const int first = u.split / (stride * kJoin) * (stride * kJoin);
-        const int members = min(kJoin, (u.splits - first + stride - 1) / stride);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (tid == 0) {
-            // Counters of the levels lie at slots of different remainders.
-            uint32_t *c = a.counters + u.slot0 + first + level;
-            const uint32_t before = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const bool last = before == (uint32_t)(members - 1);
-            if (last)
-                __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            *flag = last;
-        }
-        __syncthreads();
-        if (!*flag)
-            return;
-        const bool done = first == 0 && stride * kJoin >= u.splits;
-        for (int r = tid / PER; r < u.nrows; r += THREADS / PER) {
-            u32x2 st[kJoin];
-            u32x4 v[kJoin];
-#pragma unroll
-            for (int i = 0; i < kJoin; ++i)
-                if (i < members) {
-                    const uint32_t at = (uint32_t)(u.slot0 + first + i * stride) * SLOT;
-                    st[i] = __builtin_amdgcn_raw_buffer_load_b64(ws, at + stats + (uint32_t)r * 8u, 0, kDeviceScope);
-                    v[i] = __builtin_amdgcn_raw_buffer_load_b128(ws, at + (uint32_t)(r * DIM + d) * 4u, 0, kDeviceScope);
-                }
-            float top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kJoin; ++i)
-                if (i < members) {
-                    // (by value: a bit cast of a vector's element takes element 0)
-                    const uint32_t bits = st[i].x;
-                    top = fmaxf(top, __builtin_bit_cast(float, bits));
-                }
-            const float safe = top == -INFINITY ? 0.f : top;
-            float sum = 0.f;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < kJoin; ++i)
-                if (i < members) {
-                    const uint32_t mbits = st[i].x, lbits = st[i].y;
-                    const float f = exp2_fast(__builtin_bit_cast(float, mbits) - safe);
-                    sum += f * __builtin_bit_cast(float, lbits);
-                    acc += f * __builtin_bit_cast(f32x4, v[i]);
-                }
-            if (done) {
-                write_out<T>(a, u, u.row0 + r, d, acc, sum == 0.f ? 0.f : 1.0f / sum);
-                if (d == 0)
-                    write_lse(a, u, u.row0 + r, top, sum);
-            } else {
-                publish(first, r, d, acc, top, sum);
-            }
-        }
-        if (done)
-            return;
+                at + kStats + (uint32_t)r * 8u, 0, kDeviceScope);
     }
-}
+    // Joins slots first, first + stride, .. of one row's elements d .. d + 3:
+    // `members` of them, at most N, all loads in flight, in order.
+    template <int N>
+    __device__ __forceinline__ f32x4 join(int first, int stride, int members, int r, int d, float &top, float &sum) const
+    {
+        // The loads past the last member address the end of the workspace:
+        // out of range, they return zero without a memory access.
+        u32x2 st[N];
+        u32x4 v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t at = i < members ? (uint32_t)(first + i * stride) * kSlot : kEnd;
+            st[i] = __builtin_amdgcn_raw_buffer_load_b64(ws, at + kStats + (uint32_t)r * 8u, 0, kDeviceScope);
+            v[i] = __builtin_amdgcn_raw_buffer_load_b128(ws, at + (uint32_t)(r * DIM + d) * 4u, 0, kDeviceScope);
+        }
+        // (m and l by value: a bit cast of a vector's element takes element 0)
+        float m[N];
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t bits = st[i].x;
+            m[i] = i < members ? __builtin_bit_cast(float, bits) : -INFINITY;
+            top = fmaxf(top, m[i]);
+        }
+        const float safe = top == -INFINITY ? 0.f : top;
+        sum = 0.f;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t bits = st[i].y;
+            const float f = exp2_fast(m[i] - safe);
+            sum += f * __builtin_bit_cast(float, bits);
+            acc += f * __builtin_bit_cast(f32x4, v[i]);
+        }
+        return acc;
+    }
+};
 
 constexpr int kTilePos = 64;               // positions of the tile kernel's tiles
 
 using AttnKernel = void (*)(AttnArgs);
 // Row kernels for tiles of 16 * nb rows (nb 1, 2); nullptr if not built.
 AttnKernel attn_rows_kernel(int dtype, int dim, int nb);
-// Tile kernels for tiles of 32 * waves rows (waves 2, 4), 64 * waves threads.
+// Tile kernels for tiles of 32 * waves rows (waves 2, 4), 64 * waves threads,
+// and the kernels that join their splits, kJoinThreads threads.
 AttnKernel attn_tile_kernel(int dtype, int dim, int waves);
+AttnKernel attn_join_kernel(int dtype, int dim, int waves);
+constexpr int kJoinThreads = 256;
 
 }  // namespace gdp

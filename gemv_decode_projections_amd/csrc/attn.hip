@@ -80,6 +80,8 @@ __global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(CopyArgs a)
             *reinterpret_cast<u32x4 *>(dst + at + i * kCopyThreads * 16) = x[i];
 }
 
+constexpr int kJoinGrid = 2048;        // workgroups of the join kernel, which loop over the rows
+
 constexpr int64_t kMaxOffset = (int64_t)1 << 31;
 
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < ((int64_t)1 << 40); }
@@ -289,7 +291,7 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
     const int64_t seq_rows = (int64_t)std::min(args->max_q, batch->tokens) * a.group;
     // Up to 32 rows per sequence and key head take the row kernel, which holds
     // keys and values in registers; more take the tile kernel.
-    const void *fn;
+    const void *fn, *join = nullptr;
     int tile, threads;
     if (seq_rows <= 32) {
         const int nb = seq_rows <= 16 ? 1 : 2;
@@ -305,8 +307,9 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
         a.kv_step = kTilePos;
         a.min_split = 4 * kTilePos;
         fn = reinterpret_cast<const void *>(attn_tile_kernel(cache->dtype, cache->head_dim, waves));
+        join = reinterpret_cast<const void *>(attn_join_kernel(cache->dtype, cache->head_dim, waves));
     }
-    a.target = attn_target(tile);
+    a.target = tile == 128 ? 256 : attn_target(tile);
     // Units: one per row tile and key head, and at most `target` more.
     const int64_t tiles = (rows / tile + batch->seqs) * a.kv_heads;
     const int64_t positions = (int64_t)batch->table_width * cache->page_size;
@@ -314,7 +317,11 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
         (std::min(tiles + a.target, tiles * ((positions + a.min_split - 1) / a.min_split)) + 7) / 8 * 8;
     if (grid > 0x7fffffff)
         return PROJ_ERR_ARG;
-    return launch(fn, dim3((unsigned)grid), dim3(threads), &a, stream);
+    rc = launch(fn, dim3((unsigned)grid), dim3(threads), &a, stream);
+    // No range can be split if the longest one is not longer than a part.
+    if (rc || !join || positions <= a.min_split)
+        return rc;
+    return launch(join, dim3((unsigned)std::min<int64_t>(rows * a.kv_heads, kJoinGrid)), dim3(kJoinThreads), &a, stream);
 }
 
 }  // extern "C"

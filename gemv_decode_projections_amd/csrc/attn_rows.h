@@ -35,6 +35,8 @@ __device__ __forceinline__ void transpose8(const uint32_t (&in)[8][VEC / 2], u32
                                               j % 2 ? 0x07060302u : 0x05040100u);
 }
 
+constexpr int kJoin = 16;
+
 // Two waves per SIMD where the accumulators leave room for them.
 template <class T, int DIM, int NB>
 __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void attn_rows(AttnArgs a)
@@ -357,14 +359,64 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
             s_l[0][nb * 16 + col] = wl[nb];
         }
     __syncthreads();
-    leave_unit<T, DIM, ROWS, 256>(
-        a, u,
-        [&](auto f) {
-            const int d = 4 * (threadIdx.x % (DIM / 4));
-            for (int r = threadIdx.x / (DIM / 4); r < u.nrows; r += 256 / (DIM / 4))
-                f(r, d, *reinterpret_cast<const f32x4 *>(s_o + r * PITCH + d), s_m[0][r], s_l[0][r]);
-        },
-        &s_flag);
+    // Out of the unit: straight to the output if the tile has one split.
+    // Otherwise the rows are published in the unit's slot and the arrival is
+    // counted; the last of every kJoin consecutive splits joins those, and
+    // where there are more splits the joins are joined the same way, each
+    // result in the slot of its first split. A join thus reads at most kJoin
+    // slots, all loads in flight, and always in split order: the result does
+    // not depend on who came last. A level takes about 3 us with a tile's 16
+    // rows, as long as a second launch would.
+    constexpr int PER = DIM / 4;               // threads per row
+    const int d = 4 * (threadIdx.x % PER), r0 = threadIdx.x / PER;
+    constexpr int RSTEP = 64 * WAVES / PER;
+    auto leave = [&](int r, f32x4 v, float m, float l) {
+        write_out<T>(a, u, u.row0 + r, d, v, l == 0.f ? 0.f : 1.0f / l);
+        if (d == 0)
+            write_lse(a, u, u.row0 + r, m, l);
+    };
+    const Slots<DIM, ROWS> slots(a);
+#pragma unroll 1
+    for (int r = r0; r < u.nrows; r += RSTEP) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(s_o + r * PITCH + d);
+        if (u.splits == 1)
+            leave(r, v, s_m[0][r], s_l[0][r]);
+        else
+            slots.put(u.slot0 + u.split, r, d, v, s_m[0][r], s_l[0][r]);
+    }
+    if (u.splits == 1)
+        return;
+#pragma unroll 1
+    for (int stride = 1, level = 0;; stride *= kJoin, ++level) {
+        const int first = u.split / (stride * kJoin) * (stride * kJoin);
+        const int members = min(kJoin, (u.splits - first + stride - 1) / stride);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            // Counters of the levels lie at slots of different remainders.
+            uint32_t *c = a.counters + u.slot0 + first + level;
+            const uint32_t before = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const bool last = before == (uint32_t)(members - 1);
+            if (last)
+                __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s_flag = last;
+        }
+        __syncthreads();
+        if (!s_flag)
+            return;
+        const bool done = first == 0 && stride * kJoin >= u.splits;
+#pragma unroll 1
+        for (int r = r0; r < u.nrows; r += RSTEP) {
+            float m, l;
+            const f32x4 v = slots.template join<kJoin>(u.slot0 + first, stride, members, r, d, m, l);
+            if (done)
+                leave(r, v, m, l);
+            else
+                slots.put(u.slot0 + first, r, d, v, m, l);
+        }
+        if (done)
+            return;
+    }
 }
 
 }  // namespace gdp

@@ -66,7 +66,6 @@ __global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void 
     constexpr int STAGES = 2;
     constexpr float RAISE = 8.0f;
     __shared__ __align__(1024) char s_ring[STAGES][2][TILEB];
-    __shared__ int s_flag;
 
     AttnUnit u;
     if (!find_unit<ROWS>(a, blockIdx.x, u))
@@ -292,19 +291,91 @@ __global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void 
         }
     }
     sum = sum32(sum);
-    leave_unit<T, DIM, ROWS, 64 * WAVES>(
-        a, u,
-        [&](auto f) {
-            if (r >= u.nrows)
-                return;
+    // Out of the unit: straight to the output if the tile has one split, else
+    // to the unit's slot for the join kernel.
+    if (r >= u.nrows)
+        return;
+    const Slots<DIM, ROWS> slots(a);
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    f(r, 32 * d + 8 * g + 4 * half,
-                      f32x4{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]}, top, sum);
-        },
-        &s_flag);
+        for (int g = 0; g < 4; ++g) {
+            const int el = 32 * d + 8 * g + 4 * half;
+            const f32x4 v = {acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
+            if (u.splits == 1)
+                write_out<T>(a, u, u.row0 + r, el, v, sum == 0.f ? 0.f : 1.0f / sum);
+            else
+                slots.put(u.slot0 + u.split, r, el, v, top, sum);
+        }
+    if (u.splits == 1 && half == 0)
+        write_lse(a, u, u.row0 + r, top, sum);
+}
+
+// Joins the splits of a tile kernel's rows, one row per workgroup and pass:
+// threads in groups of DIM / 4, group g takes kJoinRun consecutive splits of
+// every kJoinThreads / (DIM / 4) * kJoinRun, each thread four elements; the
+// groups' results meet in LDS, in order. Splits of 64 to 128 rows are too much
+// for one workgroup per tile: joined in the tile kernel by the last of 16
+// workgroups they cost 30 us a level.
+constexpr int kJoinRun = 8;
+
+template <class T, int DIM, int ROWS>
+__global__ __launch_bounds__(kJoinThreads) void attn_join(AttnArgs a)
+{
+    constexpr int PER = DIM / 4;
+    constexpr int GROUPS = kJoinThreads / PER;
+    __shared__ f32x4 s_o[GROUPS][PER];
+    __shared__ float s_m[GROUPS], s_l[GROUPS];
+    Partition<ROWS> part(a);
+    auto joins = [](const Partition<ROWS> &p) { return p.joins(); };
+    const int total = part.total(joins);
+    const Slots<DIM, ROWS> slots(a);
+    const int g = threadIdx.x / PER, lane = threadIdx.x % PER;
+    for (int id = blockIdx.x; id < total; id += gridDim.x) {
+        AttnUnit u;
+        int tiles;
+        const int local = part.find(id, joins, u, tiles);
+        const int rows = u.n * a.group;
+        u.kvh = local / rows;
+        const int row = local - u.kvh * rows;
+        const int tile = row / ROWS;
+        const int first = u.slot0 + (u.kvh * tiles + tile) * u.splits;
+        float top = -INFINITY, sum = 0.f;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int s = g * kJoinRun; s < u.splits; s += GROUPS * kJoinRun) {
+            float m, l;
+            const f32x4 v = slots.template join<kJoinRun>(first + s, 1, min(kJoinRun, u.splits - s), row - tile * ROWS,
+                                                          4 * lane, m, l);
+            const float big = fmaxf(top, m), safe = big == -INFINITY ? 0.f : big;
+            const float f = exp2_fast(top - safe), h = exp2_fast(m - safe);
+            acc = acc * f + v * h;
+            sum = sum * f + l * h;
+            top = big;
+        }
+        s_o[g][lane] = acc;
+        if (lane == 0) {
+            s_m[g] = top;
+            s_l[g] = sum;
+        }
+        __syncthreads();
+        if (g == 0) {
+            const int used = min(GROUPS, (u.splits + kJoinRun - 1) / kJoinRun);
+            for (int i = 1; i < used; ++i)
+                top = fmaxf(top, s_m[i]);
+            const float safe = top == -INFINITY ? 0.f : top;
+            acc = f32x4{0.f, 0.f, 0.f, 0.f};
+            sum = 0.f;
+            for (int i = 0; i < used; ++i) {
+                const float f = exp2_fast(s_m[i] - safe);
+                acc += s_o[i][lane] * f;
+                sum += s_l[i] * f;
+            }
+            write_out<T>(a, u, row, 4 * lane, acc, sum == 0.f ? 0.f : 1.0f / sum);
+            if (lane == 0)
+                write_lse(a, u, row, top, sum);
+        }
+        __syncthreads();
+    }
 }
 
 }  // namespace gdp

@@ -107,7 +107,7 @@ int blk_kv_copy_pages(const blk_cache *cache, const int32_t *src, const int32_t 
  *   ws: blk_attn_workspace_bytes(head_dim) bytes, 256-byte aligned, zeroed
  *       before the first use; the kernels leave it ready for the next call.
  *       Calls that can overlap need workspaces of their own.
- * Exactly one launch (none if seqs or tokens is 0).
+ * One launch, or two (none if seqs or tokens is 0).
  */
 typedef struct {
     const void *q;
