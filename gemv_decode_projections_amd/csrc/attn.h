@@ -13,6 +13,22 @@
 
 namespace gdp {
 
+// Division by a number the host knows, exact below 2^31: x * ceil(2^p / d) >>
+// p with p = 31 + ceil(log2 d).
+struct Divisor {
+    uint32_t mul;
+    int shift;
+
+    static Divisor of(uint32_t d)
+    {
+        int s = 0;
+        while (((uint64_t)1 << s) < d)
+            ++s;
+        return {(uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d), 31 + s};
+    }
+    __device__ __forceinline__ int operator()(int x) const { return (int)((uint64_t)(uint32_t)x * mul >> shift); }
+};
+
 struct AttnArgs {
     const char *k, *v;                 // cache
     uint32_t page_stride;              // bytes
@@ -27,11 +43,12 @@ struct AttnArgs {
     int64_t q_stride, gate_stride, out_stride;     // bytes
     int64_t q_head, gate_head, out_head;           // bytes
     int heads, kv_heads, group;
+    Divisor by_heads, by_group;        // of kv_heads and group
     int window;
     float scale_log2;                  // scale * log2(e): softmax in base 2
-    int kv_step;                       // split lengths are multiples of this
+    int kv_step;                       // split lengths are multiples of this (a power of two)
     int min_split;                     // smallest split length
-    int target;                        // units aimed at when rows alone are too few
+    float per_target;                  // 1 / units aimed at when rows alone are too few
     char *slots;                       // partials
     uint32_t *counters;                // one per slot, zero between launches
 };
@@ -106,51 +123,62 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, 
 template <int ROWS>
 struct Partition {
     struct Shape {
-        int tok0, n, len, tiles, first, range;
+        int tok0, n, len, tiles, first, range, splits;
     };
     const AttnArgs &a;
     Shape s;             // the lane's sequence of the last 64 looked at
     int c;
+    float per_c;
 
-    __device__ Shape shape(int b) const
+    __device__ void shape(int b)
     {
-        Shape x = {0, 0, 0, 0, 0, 0};
+        s = Shape{0, 0, 0, 0, 0, 0, 1};
         if (b < a.seqs) {
-            seq_bounds(a, b, x.tok0, x.n, x.len);
-            x.tiles = (x.n * a.group + ROWS - 1) / ROWS;
+            seq_bounds(a, b, s.tok0, s.n, s.len);
+            s.tiles = (s.n * a.group + ROWS - 1) / ROWS;
             if (a.window > 0)
-                x.first = max(0, x.len - x.n - a.window + 1) / a.kv_step * a.kv_step;
-            x.range = x.len - x.first;
+                s.first = max(0, s.len - s.n - a.window + 1) & -a.kv_step;
+            s.range = s.len - s.first;
         }
-        return x;
+    }
+    // ceil(range / c): the FP32 quotient is at most one off.
+    __device__ void cut()
+    {
+        int q = (int)((float)(s.range + c - 1) * per_c);
+        q += q * c < s.range ? 1 : 0;
+        q -= (q - 1) * c >= s.range ? 1 : 0;
+        s.splits = max(q, 1);
     }
     __device__ explicit Partition(const AttnArgs &args) : a(args)
     {
         unsigned long long w = 0;
         for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
-            s = shape(b0 + (int)(threadIdx.x % kWave));
+            shape(b0 + (int)(threadIdx.x % kWave));
             w += (unsigned long long)s.tiles * (unsigned)s.range;
         }
         w = wave_scan(w);
-        w = ((unsigned long long)(unsigned)last_lane((int)(w >> 32)) << 32 | (unsigned)last_lane((int)w)) *
-            (unsigned)a.kv_heads;
-        const unsigned long long per = (w + a.target - 1) / a.target;
-        c = (int)min((unsigned long long)0x40000000,
-                     max((unsigned long long)a.min_split, (per + a.kv_step - 1) / a.kv_step * a.kv_step));
+        // Rounded up past the error of FP32: a larger c only means fewer parts.
+        const float all = ((float)(unsigned)last_lane((int)(w >> 32)) * 0x1p32f + (float)(unsigned)last_lane((int)w)) *
+                          (float)a.kv_heads;
+        const int per = (int)fminf(all * a.per_target * 1.00001f + 1.0f, 0x1p29f);
+        c = __builtin_amdgcn_readfirstlane(max(a.min_split, (per + a.kv_step - 1) & -a.kv_step));
+        per_c = 1.0f / (float)c;
+        cut();
     }
-    __device__ int splits() const { return max(1, (s.range + c - 1) / c); }
-    __device__ int units() const { return s.tiles * splits() * a.kv_heads; }
-    __device__ int slots() const { return splits() > 1 ? units() : 0; }
+    __device__ int units() const { return s.tiles * s.splits * a.kv_heads; }
+    __device__ int slots() const { return s.splits > 1 ? units() : 0; }
     // Rows whose splits have to be joined.
-    __device__ int joins() const { return splits() > 1 ? s.n * a.group * a.kv_heads : 0; }
+    __device__ int joins() const { return s.splits > 1 ? s.n * a.group * a.kv_heads : 0; }
 
     template <class Count>
     __device__ int total(Count count)
     {
         int t = 0;
         for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
-            if (a.seqs > kWave)
-                s = shape(b0 + (int)(threadIdx.x % kWave));
+            if (a.seqs > kWave) {
+                shape(b0 + (int)(threadIdx.x % kWave));
+                cut();
+            }
             t += count(*this);
         }
         return last_lane(wave_scan(t));
@@ -163,8 +191,10 @@ struct Partition {
     {
         int items_before = 0, slots_before = 0;
         for (int b0 = 0;; b0 += kWave) {
-            if (a.seqs > kWave)
-                s = shape(b0 + (int)(threadIdx.x % kWave));
+            if (a.seqs > kWave) {
+                shape(b0 + (int)(threadIdx.x % kWave));
+                cut();
+            }
             const int isum = items_before + wave_scan(count(*this));
             const int ssum = slots_before + wave_scan(slots());
             const unsigned long long mine = __ballot(isum > want);
@@ -175,7 +205,7 @@ struct Partition {
                 u.tok0 = of(s.tok0);
                 u.n = of(s.n);
                 u.len = of(s.len);
-                u.splits = of(splits());
+                u.splits = of(s.splits);
                 u.lo = of(s.first);
                 u.slot0 = of(ssum - slots());
                 tiles = of(s.tiles);
@@ -205,15 +235,22 @@ __device__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
         return false;
     int tiles;
     const int local = part.find(want, units, u, tiles);
-    const int tile = local % tiles;
-    u.kvh = local / tiles % a.kv_heads;
-    u.split = local / tiles / a.kv_heads;
+    int tile = 0, rest = local;
+    if (tiles > 1) {
+        rest = local / tiles;
+        tile = local - rest * tiles;
+    }
+    u.split = a.by_heads(rest);
+    u.kvh = rest - u.split * a.kv_heads;
     u.slot0 += (u.kvh * tiles + tile) * u.splits;
+    // Offsets that do not ascend could ask for more slots than there are.
+    if (u.splits > 1 && (unsigned)(u.slot0 + u.splits) > (unsigned)kAttnSlotRows / ROWS)
+        return false;
     u.row0 = tile * ROWS;
     u.nrows = min(ROWS, u.n * a.group - u.row0);
     u.lo += u.split * part.c;
     // The tile's last token sees no further than its own position.
-    const int last = u.len - u.n + (u.row0 + u.nrows - 1) / a.group;
+    const int last = u.len - u.n + a.by_group(u.row0 + u.nrows - 1);
     u.hi = min(u.split + 1 < u.splits ? u.lo + part.c : u.len, max(last + 1, 0));
     return true;
 }
@@ -231,15 +268,26 @@ __device__ __forceinline__ bool kv_offset(const AttnArgs &a, int page, int p, in
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + exp2_fast(-1.44269504f * x)); }
 
-// Writes four consecutive outputs of a row: divided, gated, rounded once.
-template <class T>
-__device__ __forceinline__ void write_out(const AttnArgs &a, const AttnUnit &u, int row, int d, f32x4 o, float inv)
+// Token and query head of a row.
+__device__ __forceinline__ void row_place(const AttnArgs &a, const AttnUnit &u, int row, int &tok, int &head)
 {
-    const int tok = u.tok0 + row / a.group;
-    const int head = u.kvh * a.group + row % a.group;
-    o *= inv;
+    const int i = a.by_group(row);
+    tok = u.tok0 + i;
+    head = u.kvh * a.group + row - i * a.group;
+}
+
+// The gate's four elements for outputs d .. d + 3 of a row.
+__device__ __forceinline__ u32x2 load_gate(const AttnArgs &a, int tok, int head, int d)
+{
+    return *reinterpret_cast<const u32x2 *>(a.gate + tok * a.gate_stride + head * a.gate_head + d * 2);
+}
+
+// Writes four consecutive outputs of a row: divided by the sum, gated, rounded once.
+template <class T>
+__device__ __forceinline__ void write_out(const AttnArgs &a, int tok, int head, int d, f32x4 o, float sum, u32x2 g)
+{
+    o *= sum == 0.f ? 0.f : 1.0f / sum;
     if (a.gate) {
-        const u32x2 g = *reinterpret_cast<const u32x2 *>(a.gate + tok * a.gate_stride + head * a.gate_head + d * 2);
         o.x *= sigmoid(T::lo(g.x));
         o.y *= sigmoid(T::hi(g.x));
         o.z *= sigmoid(T::lo(g.y));
@@ -249,10 +297,10 @@ __device__ __forceinline__ void write_out(const AttnArgs &a, const AttnUnit &u, 
         u32x2{T::pack(o.x, o.y), T::pack(o.z, o.w)};
 }
 
-__device__ __forceinline__ void write_lse(const AttnArgs &a, const AttnUnit &u, int row, float m, float l)
+__device__ __forceinline__ void write_lse(const AttnArgs &a, int tok, int head, float m, float l)
 {
     if (a.lse)
-        a.lse[(int64_t)(u.tok0 + row / a.group) * a.heads + u.kvh * a.group + row % a.group] =
+        a.lse[(int64_t)tok * a.heads + head] =
             l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * 0.693147181f : -INFINITY;
 }
 

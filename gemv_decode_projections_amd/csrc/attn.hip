@@ -283,6 +283,8 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
     a.out_head = args->out_head_stride * 2;
     a.heads = args->heads;
     a.group = args->heads / cache->kv_heads;
+    a.by_group = Divisor::of(a.group);
+    a.by_heads = Divisor::of(a.kv_heads);
     a.window = std::min(args->window, 0x3fffffff);
     a.scale_log2 = args->scale * 1.44269504f;
     a.counters = static_cast<uint32_t *>(ws);
@@ -309,12 +311,13 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
         fn = reinterpret_cast<const void *>(attn_tile_kernel(cache->dtype, cache->head_dim, waves));
         join = reinterpret_cast<const void *>(attn_join_kernel(cache->dtype, cache->head_dim, waves));
     }
-    a.target = tile == 128 ? 256 : attn_target(tile);
+    const int target = tile == 128 ? 256 : attn_target(tile);
+    a.per_target = 1.0f / (float)target;
     // Units: one per row tile and key head, and at most `target` more.
     const int64_t tiles = (rows / tile + batch->seqs) * a.kv_heads;
     const int64_t positions = (int64_t)batch->table_width * cache->page_size;
     const int64_t grid =
-        (std::min(tiles + a.target, tiles * ((positions + a.min_split - 1) / a.min_split)) + 7) / 8 * 8;
+        (std::min(tiles + target, tiles * ((positions + a.min_split - 1) / a.min_split)) + 7) / 8 * 8;
     if (grid > 0x7fffffff)
         return PROJ_ERR_ARG;
     rc = launch(fn, dim3((unsigned)grid), dim3(threads), &a, stream);

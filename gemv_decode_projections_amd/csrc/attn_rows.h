@@ -48,8 +48,12 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
     constexpr int HALF = DIM / (16 * VEC);           // 16 * VEC element blocks of a value row
     constexpr int PITCH = DIM + 4;
     constexpr int STEP = 32;
-    __shared__ __align__(16) float s_o[ROWS * PITCH];
+    constexpr int PER = DIM / 4;               // threads per row when rows leave
+    constexpr int RSTEP = 64 * WAVES / PER;    // rows per pass then
+    constexpr int PASSES = (ROWS + RSTEP - 1) / RSTEP;
+    __shared__ __align__(16) float s_o[WAVES][ROWS * PITCH];
     __shared__ float s_m[WAVES][ROWS], s_l[WAVES][ROWS];
+    __shared__ u32x2 s_gate[PASSES][64 * WAVES];
     __shared__ int s_flag;
 
     AttnUnit u;
@@ -66,19 +70,18 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const int r = nb * 16 + col;
-        const int row = u.row0 + min(r, u.nrows - 1);
-        const int i = row / a.group;
-        const int head = u.kvh * a.group + row - i * a.group;
-        const char *p = a.q + (int64_t)(u.tok0 + i) * a.q_stride + head * a.q_head + quad * 16;
+        int tok, head;
+        row_place(a, u, u.row0 + min(r, u.nrows - 1), tok, head);
+        const char *p = a.q + tok * a.q_stride + head * a.q_head + quad * 16;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
             qf[nb][ks] = *reinterpret_cast<const u32x4 *>(p + ks * 64);
-        const int pos = u.len - u.n + i;
+        const int pos = u.len - u.n + tok - u.tok0;
         see_hi[nb] = r < u.nrows ? pos + 1 : 0;
         see_lo[nb] = a.window > 0 ? pos - a.window + 1 : 0;
     }
     // Positions that every row of the tile sees need no mask.
-    const int i0 = u.row0 / a.group, i1 = (u.row0 + u.nrows - 1) / a.group;
+    const int i0 = a.by_group(u.row0), i1 = a.by_group(u.row0 + u.nrows - 1);
     const int all_hi = u.len - u.n + i0 + 1;
     const int all_lo = a.window > 0 ? u.len - u.n + i1 - a.window + 1 : 0;
 
@@ -156,6 +159,15 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
         load_k(base, pg);
         load_v(base, pg);
     }
+    // The gate waits in LDS for the end, read by the thread that will use it.
+    const int d = 4 * (threadIdx.x % PER), r0 = threadIdx.x / PER;
+    if (a.gate)
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k) {
+            int tok, head;
+            row_place(a, u, u.row0 + min(r0 + k * RSTEP, u.nrows - 1), tok, head);
+            s_gate[k][threadIdx.x] = load_gate(a, tok, head, d);
+        }
     for (; base < u.hi; base += WAVES * STEP) {
         const int after = base + WAVES * STEP;
         f32x4 s[NB][2];
@@ -296,69 +308,26 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
         next = coming;
     }
 
-    // Join the waves. Each scales its rows to the workgroup's maximum; then
-    // they add their parts into LDS in four turns, each turn a different
-    // quarter of the elements per wave.
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        sum[nb] = sum_quads(sum[nb]);
-        if (quad == 0) {
-            s_m[wave][nb * 16 + col] = top[nb];
-            s_l[wave][nb * 16 + col] = sum[nb];
-        }
-    }
-    __syncthreads();
-    float wm[NB], wl[NB];
+    // Join the waves: each leaves its rows, maxima and sums in LDS.
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const int r = nb * 16 + col;
-        float m = s_m[0][r];
-#pragma unroll
-        for (int w = 1; w < WAVES; ++w)
-            m = fmaxf(m, s_m[w][r]);
-        const float safe = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w)
-            l += s_l[w][r] * exp2_fast(s_m[w][r] - safe);
-        wm[nb] = m;
-        wl[nb] = l;
-        const float f = exp2_fast(top[nb] - safe);
+        sum[nb] = sum_quads(sum[nb]);
+        if (quad == 0) {
+            s_m[wave][r] = top[nb];
+            s_l[wave][r] = sum[nb];
+        }
 #pragma unroll
         for (int h = 0; h < HALF; ++h)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                acc[nb][h][j] *= f;
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; j += 4)
+                    *reinterpret_cast<f32x4 *>(s_o[wave] + r * PITCH + h * 16 * VEC + VEC * (4 * quad + i) + j) =
+                        f32x4{acc[nb][h][j][i], acc[nb][h][j + 1][i], acc[nb][h][j + 2][i], acc[nb][h][j + 3][i]};
     }
-    for (int turn = 0; turn < WAVES; ++turn) {
-        const int mine = (wave + turn) % WAVES;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i != mine)
-                continue;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int h = 0; h < HALF; ++h)
-#pragma unroll
-                    for (int j = 0; j < VEC; j += 4) {
-                        f32x4 *p = reinterpret_cast<f32x4 *>(s_o + (nb * 16 + col) * PITCH + h * 16 * VEC +
-                                                             VEC * (4 * quad + i) + j);
-                        f32x4 x = {acc[nb][h][j][i], acc[nb][h][j + 1][i], acc[nb][h][j + 2][i], acc[nb][h][j + 3][i]};
-                        if (turn > 0)
-                            x += *p;
-                        *p = x;
-                    }
-        }
-        __syncthreads();
-    }
-    if (wave == 0 && quad == 0)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            s_m[0][nb * 16 + col] = wm[nb];
-            s_l[0][nb * 16 + col] = wl[nb];
-        }
     __syncthreads();
+
     // Out of the unit: straight to the output if the tile has one split.
     // Otherwise the rows are published in the unit's slot and the arrival is
     // counted; the last of every kJoin consecutive splits joins those, and
@@ -367,22 +336,33 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
     // slots, all loads in flight, and always in split order: the result does
     // not depend on who came last. A level takes about 3 us with a tile's 16
     // rows, as long as a second launch would.
-    constexpr int PER = DIM / 4;               // threads per row
-    const int d = 4 * (threadIdx.x % PER), r0 = threadIdx.x / PER;
-    constexpr int RSTEP = 64 * WAVES / PER;
     auto leave = [&](int r, f32x4 v, float m, float l) {
-        write_out<T>(a, u, u.row0 + r, d, v, l == 0.f ? 0.f : 1.0f / l);
+        int tok, head;
+        row_place(a, u, u.row0 + r, tok, head);
+        write_out<T>(a, tok, head, d, v, l, a.gate ? s_gate[(r - r0) / RSTEP][threadIdx.x] : u32x2{0, 0});
         if (d == 0)
-            write_lse(a, u, u.row0 + r, m, l);
+            write_lse(a, tok, head, m, l);
     };
     const Slots<DIM, ROWS> slots(a);
 #pragma unroll 1
     for (int r = r0; r < u.nrows; r += RSTEP) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(s_o + r * PITCH + d);
+        float m = s_m[0][r];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w)
+            m = fmaxf(m, s_m[w][r]);
+        const float safe = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float f = exp2_fast(s_m[w][r] - safe);
+            l += f * s_l[w][r];
+            v += f * *reinterpret_cast<const f32x4 *>(s_o[w] + r * PITCH + d);
+        }
         if (u.splits == 1)
-            leave(r, v, s_m[0][r], s_l[0][r]);
+            leave(r, v, m, l);
         else
-            slots.put(u.slot0 + u.split, r, d, v, s_m[0][r], s_l[0][r]);
+            slots.put(u.slot0 + u.split, r, d, v, m, l);
     }
     if (u.splits == 1)
         return;

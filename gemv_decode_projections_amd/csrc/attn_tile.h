@@ -77,20 +77,18 @@ __global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void 
     // Queries as B operands; rows past the last read it again and see nothing.
     u32x4 qf[KS];
     const int r = wave * 32 + col;
-    int see_lo, see_hi;
+    int see_lo, see_hi, tok, head;
     {
-        const int row = u.row0 + min(r, u.nrows - 1);
-        const int i = row / a.group;
-        const int head = u.kvh * a.group + row - i * a.group;
-        const char *p = a.q + (int64_t)(u.tok0 + i) * a.q_stride + head * a.q_head + half * 16;
+        row_place(a, u, u.row0 + min(r, u.nrows - 1), tok, head);
+        const char *p = a.q + tok * a.q_stride + head * a.q_head + half * 16;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
             qf[ks] = *reinterpret_cast<const u32x4 *>(p + ks * 32);
-        const int pos = u.len - u.n + i;
+        const int pos = u.len - u.n + tok - u.tok0;
         see_hi = r < u.nrows ? pos + 1 : 0;
         see_lo = a.window > 0 ? pos - a.window + 1 : 0;
     }
-    const int i0 = u.row0 / a.group, i1 = (u.row0 + u.nrows - 1) / a.group;
+    const int i0 = a.by_group(u.row0), i1 = a.by_group(u.row0 + u.nrows - 1);
     const int all_hi = u.len - u.n + i0 + 1;
     const int all_lo = a.window > 0 ? u.len - u.n + i1 - a.window + 1 : 0;
 
@@ -303,12 +301,12 @@ __global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void 
             const int el = 32 * d + 8 * g + 4 * half;
             const f32x4 v = {acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
             if (u.splits == 1)
-                write_out<T>(a, u, u.row0 + r, el, v, sum == 0.f ? 0.f : 1.0f / sum);
+                write_out<T>(a, tok, head, el, v, sum, a.gate ? load_gate(a, tok, head, el) : u32x2{0, 0});
             else
                 slots.put(u.slot0 + u.split, r, el, v, top, sum);
         }
     if (u.splits == 1 && half == 0)
-        write_lse(a, u, u.row0 + r, top, sum);
+        write_lse(a, tok, head, top, sum);
 }
 
 // Joins the splits of a tile kernel's rows, one row per workgroup and pass:
@@ -340,6 +338,9 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join(AttnArgs a)
         const int row = local - u.kvh * rows;
         const int tile = row / ROWS;
         const int first = u.slot0 + (u.kvh * tiles + tile) * u.splits;
+        int tok, head;
+        row_place(a, u, row, tok, head);
+        const u32x2 gate = a.gate ? load_gate(a, tok, head, 4 * lane) : u32x2{0, 0};
         float top = -INFINITY, sum = 0.f;
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
         for (int s = g * kJoinRun; s < u.splits; s += GROUPS * kJoinRun) {
@@ -370,9 +371,9 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join(AttnArgs a)
                 acc += s_o[i][lane] * f;
                 sum += s_l[i] * f;
             }
-            write_out<T>(a, u, row, 4 * lane, acc, sum == 0.f ? 0.f : 1.0f / sum);
+            write_out<T>(a, tok, head, 4 * lane, acc, sum, gate);
             if (lane == 0)
-                write_lse(a, u, row, top, sum);
+                write_lse(a, tok, head, top, sum);
         }
         __syncthreads();
     }
