@@ -31,6 +31,7 @@ SOURCES = [
     "attn.hip",
     "attn_rows.hip",
     "attn_tile.hip",
+    "attn_join.hip",
     "w4.hip",
     "norm.hip",
 ]

@@ -48,7 +48,9 @@ struct AttnArgs {
     float scale_log2;                  // scale * log2(e): softmax in base 2
     int kv_step;                       // split lengths are multiples of this (a power of two)
     int min_split;                     // smallest split length
-    float per_target;                  // 1 / units aimed at when rows alone are too few
+    int target;                        // workgroups the chip holds at once
+    float per_target;                  // 1 / target
+    int rounds;                        // of them, where one round would not be even
     char *slots;                       // partials
     uint32_t *counters;                // one per slot, zero between launches
 };
@@ -56,16 +58,11 @@ struct AttnArgs {
 // A split's partial result takes a slot: its rows' FP32 outputs, maxima and
 // sums. Splits that share row tiles number at most two per unit aimed at (a
 // tile's range r is cut in ceil(r / C) parts; where that is more than one it
-// is less than 2 r / C, and the ranges sum to at most target * C), so the
-// kernels aim at units in inverse proportion to their tile's rows and one
-// workspace serves all of them.
+// is less than 2 r / C, and the ranges sum to at most target * C), so kernels
+// whose tiles have more rows aim at fewer units, and one workspace serves all.
 constexpr int kAttnSlotRows = 131072;              // rows of all slots together
-constexpr int kAttnMaxTarget = 512;
-__host__ __device__ constexpr int attn_target(int rows)
-{
-    return kAttnSlotRows / 2 / rows < kAttnMaxTarget ? kAttnSlotRows / 2 / rows : kAttnMaxTarget;
-}
-constexpr size_t kAttnCounterBytes = 2 * kAttnMaxTarget * sizeof(uint32_t);
+constexpr int kAttnMaxSlots = kAttnSlotRows / 16;
+constexpr size_t kAttnCounterBytes = kAttnMaxSlots * sizeof(uint32_t);
 constexpr size_t attn_ws_bytes(int dim) { return kAttnCounterBytes + (size_t)kAttnSlotRows * (dim + 2) * 4; }
 
 // One workgroup's share: rows row0 .. row0 + nrows - 1 of sequence `seq`
@@ -102,6 +99,17 @@ __device__ __forceinline__ I wave_scan(I x)
     x += lane_moved<0x143, 0xc>(x);
     return x;
 }
+// The largest of the lanes' values, none negative.
+__device__ __forceinline__ int wave_max(int x)
+{
+    x = max(x, lane_moved<0x111, 0xf>(x));
+    x = max(x, lane_moved<0x112, 0xf>(x));
+    x = max(x, lane_moved<0x114, 0xf>(x));
+    x = max(x, lane_moved<0x118, 0xf>(x));
+    x = max(x, lane_moved<0x142, 0xa>(x));
+    x = max(x, lane_moved<0x143, 0xc>(x));
+    return __builtin_amdgcn_readlane(x, kWave - 1);
+}
 __device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, kWave - 1); }
 
 // New tokens and cached positions of sequence b, bounded to the tensors.
@@ -115,11 +123,20 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, 
     len = (int)min((int64_t)max(a.kv_len[b], 0), cap);
 }
 
-// Partition: with W = the row tiles' ranges summed over sequences and heads,
-// every tile's range is cut in parts of C = max(min_split, W / target)
-// positions, so a batch of any mix of lengths gives about `target` equal
-// units, or one per tile where there are many tiles. Every workgroup computes
-// the same partition from the device's lengths, one lane per sequence.
+// Partition. Every tile's range is cut in parts of C positions. Every
+// workgroup computes the same partition from the device's lengths, one lane
+// per sequence. With W the row tiles' ranges summed over sequences and heads
+// and `target` the workgroups the chip holds at once, C is W / target: about
+// one unit for each of them, or one per tile where there are many tiles. The
+// row kernels refine that:
+//   - the last part of a tile is short, so there are more units than
+//     W / C: C is raised until they fit one round (32 sequences of up to 8192
+//     positions x 8 heads: 640 units in 512 places took 139 us, 512 in 128);
+//   - with much work per unit, or more tiles than half the places, several
+//     rounds of smaller parts even out better (2048 units: 121 us);
+//   - short parts are not worth a join: up to 512 positions per part as long
+//     as a tile has no more than 16 parts and half the places are taken (one
+//     token over 131072 positions: 256 parts 20.5 us, 512 parts 24).
 template <int ROWS>
 struct Partition {
     struct Shape {
@@ -152,16 +169,39 @@ struct Partition {
     __device__ explicit Partition(const AttnArgs &args) : a(args)
     {
         unsigned long long w = 0;
+        int t = 0, longest = 0;
         for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
             shape(b0 + (int)(threadIdx.x % kWave));
             w += (unsigned long long)s.tiles * (unsigned)s.range;
+            t += s.tiles;
+            longest = max(longest, s.range);
         }
         w = wave_scan(w);
         // Rounded up past the error of FP32: a larger c only means fewer parts.
         const float all = ((float)(unsigned)last_lane((int)(w >> 32)) * 0x1p32f + (float)(unsigned)last_lane((int)w)) *
-                          (float)a.kv_heads;
-        const int per = (int)fminf(all * a.per_target * 1.00001f + 1.0f, 0x1p29f);
-        c = __builtin_amdgcn_readfirstlane(max(a.min_split, (per + a.kv_step - 1) & -a.kv_step));
+                          (float)a.kv_heads * 1.00001f;
+        float per = all * a.per_target;
+        if (ROWS <= 32) {
+            const float tiles = (float)last_lane(wave_scan(t)) * (float)a.kv_heads;
+            const bool even = per < 2048.f && tiles <= 0.5f * (float)a.target;
+            if (!even)
+                per /= (float)a.rounds;
+            set_part(fmaxf(per, fminf(512.f, fmaxf((float)wave_max(longest) * (1.f / 16), all * a.per_target * 2.f))));
+            if (even && a.seqs <= kWave)
+                for (int i = 0; i < 2; ++i) {
+                    const int n = last_lane(wave_scan(units()));
+                    if (n <= a.target)
+                        break;
+                    set_part((float)c * (float)n * a.per_target);
+                }
+        } else {
+            set_part(per);
+        }
+    }
+    __device__ void set_part(float positions)
+    {
+        const int p = (int)fminf(positions + 1.0f, 0x1p29f);
+        c = __builtin_amdgcn_readfirstlane(max(a.min_split, (p + a.kv_step - 1) & -a.kv_step));
         per_c = 1.0f / (float)c;
         cut();
     }
@@ -370,10 +410,10 @@ constexpr int kTilePos = 64;               // positions of the tile kernel's til
 using AttnKernel = void (*)(AttnArgs);
 // Row kernels for tiles of 16 * nb rows (nb 1, 2); nullptr if not built.
 AttnKernel attn_rows_kernel(int dtype, int dim, int nb);
-// Tile kernels for tiles of 32 * waves rows (waves 2, 4), 64 * waves threads,
-// and the kernels that join their splits, kJoinThreads threads.
+// Tile kernels for tiles of 32 * waves rows (waves 2, 4), 64 * waves threads.
 AttnKernel attn_tile_kernel(int dtype, int dim, int waves);
-AttnKernel attn_join_kernel(int dtype, int dim, int waves);
+// Join kernels for tiles of 16, 32, 64 or 128 rows, kJoinThreads threads.
+AttnKernel attn_join_kernel(int dtype, int dim, int rows);
 constexpr int kJoinThreads = 256;
 
 }  // namespace gdp

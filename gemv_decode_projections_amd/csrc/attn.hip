@@ -293,14 +293,21 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
     const int64_t seq_rows = (int64_t)std::min(args->max_q, batch->tokens) * a.group;
     // Up to 32 rows per sequence and key head take the row kernel, which holds
     // keys and values in registers; more take the tile kernel.
+    // The row kernel counts the joins of its tiles of 16 rows itself; the
+    // others' are a second launch.
     const void *fn, *join = nullptr;
     int tile, threads;
+    a.rounds = 1;
     if (seq_rows <= 32) {
         const int nb = seq_rows <= 16 ? 1 : 2;
         tile = 16 * nb;
         threads = 256;
         a.kv_step = 128;
         a.min_split = 128;
+        // Two workgroups per compute unit; one where a head's 256 elements
+        // take all registers, four of 64 elements.
+        a.target = cache->head_dim == 64 ? 1024 : cache->head_dim == 128 ? 512 : 256;
+        a.rounds = 4 / nb;
         fn = reinterpret_cast<const void *>(attn_rows_kernel(cache->dtype, cache->head_dim, nb));
     } else {
         const int waves = seq_rows <= 64 ? 2 : 4;
@@ -308,16 +315,20 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
         threads = 64 * waves;
         a.kv_step = kTilePos;
         a.min_split = 4 * kTilePos;
+        // Splits of 128 rows cost more than an uneven round.
+        a.target = waves == 2 ? 512 : 256;
         fn = reinterpret_cast<const void *>(attn_tile_kernel(cache->dtype, cache->head_dim, waves));
-        join = reinterpret_cast<const void *>(attn_join_kernel(cache->dtype, cache->head_dim, waves));
     }
-    const int target = tile == 128 ? 256 : attn_target(tile);
-    a.per_target = 1.0f / (float)target;
-    // Units: one per row tile and key head, and at most `target` more.
+    if (tile > 16)
+        join = reinterpret_cast<const void *>(attn_join_kernel(cache->dtype, cache->head_dim, tile));
+    a.per_target = 1.0f / (float)a.target;
+    // Units: one per row tile and key head, and at most `target` more, times
+    // the rounds if the most work there can be asks for them.
     const int64_t tiles = (rows / tile + batch->seqs) * a.kv_heads;
     const int64_t positions = (int64_t)batch->table_width * cache->page_size;
-    const int64_t grid =
-        (std::min(tiles + target, tiles * ((positions + a.min_split - 1) / a.min_split)) + 7) / 8 * 8;
+    const int64_t more =
+        tiles * positions >= (int64_t)2048 * a.target || tiles > a.target / 2 ? a.target * a.rounds : a.target;
+    const int64_t grid = (std::min(tiles + more, tiles * ((positions + a.min_split - 1) / a.min_split)) + 7) / 8 * 8;
     if (grid > 0x7fffffff)
         return PROJ_ERR_ARG;
     rc = launch(fn, dim3((unsigned)grid), dim3(threads), &a, stream);

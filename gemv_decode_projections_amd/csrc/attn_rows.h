@@ -329,13 +329,15 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
     __syncthreads();
 
     // Out of the unit: straight to the output if the tile has one split.
-    // Otherwise the rows are published in the unit's slot and the arrival is
-    // counted; the last of every kJoin consecutive splits joins those, and
-    // where there are more splits the joins are joined the same way, each
-    // result in the slot of its first split. A join thus reads at most kJoin
-    // slots, all loads in flight, and always in split order: the result does
-    // not depend on who came last. A level takes about 3 us with a tile's 16
-    // rows, as long as a second launch would.
+    // Otherwise the rows are published in the unit's slot. With 32 rows a
+    // second launch joins them. With 16 the arrival is counted; the last of
+    // every kJoin consecutive splits joins those, and where there are more
+    // splits the joins are joined the same way, each result in the slot of its
+    // first split. A join thus reads at most kJoin slots, all loads in flight,
+    // and always in split order: the result does not depend on who came last.
+    // (One token over 1000 positions: 9.7 us, with the second launch 12.4; 24
+    // rows x 16 sequences of up to 16384 positions: 24.7 to 39 us, with the
+    // second launch 20.)
     auto leave = [&](int r, f32x4 v, float m, float l) {
         int tok, head;
         row_place(a, u, u.row0 + r, tok, head);
@@ -364,7 +366,7 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
         else
             slots.put(u.slot0 + u.split, r, d, v, m, l);
     }
-    if (u.splits == 1)
+    if (u.splits == 1 || NB > 1)
         return;
 #pragma unroll 1
     for (int stride = 1, level = 0;; stride *= kJoin, ++level) {
@@ -388,7 +390,9 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
 #pragma unroll 1
         for (int r = r0; r < u.nrows; r += RSTEP) {
             float m, l;
-            const f32x4 v = slots.template join<kJoin>(u.slot0 + first, stride, members, r, d, m, l);
+            const f32x4 v =
+                members <= kJoin / 2 ? slots.template join<kJoin / 2>(u.slot0 + first, stride, members, r, d, m, l)
+                                     : slots.template join<kJoin>(u.slot0 + first, stride, members, r, d, m, l);
             if (done)
                 leave(r, v, m, l);
             else

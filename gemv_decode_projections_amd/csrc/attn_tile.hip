@@ -9,21 +9,6 @@ static AttnKernel pick(int waves)
     return waves == 2 ? attn_tile<T, DIM, 2> : waves == 4 ? attn_tile<T, DIM, 4> : nullptr;
 }
 
-template <class T, int DIM>
-static AttnKernel pick_join(int waves)
-{
-    return waves == 2 ? attn_join<T, DIM, 64> : waves == 4 ? attn_join<T, DIM, 128> : nullptr;
-}
-
-template <class T>
-static AttnKernel pick_join(int dim, int waves)
-{
-    return dim == 64    ? pick_join<T, 64>(waves)
-           : dim == 128 ? pick_join<T, 128>(waves)
-           : dim == 256 ? pick_join<T, 256>(waves)
-                        : nullptr;
-}
-
 template <class T>
 static AttnKernel pick(int dim, int waves)
 {
@@ -33,11 +18,6 @@ static AttnKernel pick(int dim, int waves)
 AttnKernel attn_tile_kernel(int dtype, int dim, int waves)
 {
     return dtype == BLK_BF16 ? pick<BF16>(dim, waves) : dtype == BLK_F16 ? pick<F16>(dim, waves) : nullptr;
-}
-
-AttnKernel attn_join_kernel(int dtype, int dim, int waves)
-{
-    return dtype == BLK_BF16 ? pick_join<BF16>(dim, waves) : dtype == BLK_F16 ? pick_join<F16>(dim, waves) : nullptr;
 }
 
 }  // namespace gdp
