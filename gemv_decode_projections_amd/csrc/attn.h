@@ -126,17 +126,18 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, 
 // Partition. Every tile's range is cut in parts of C positions. Every
 // workgroup computes the same partition from the device's lengths, one lane
 // per sequence. With W the row tiles' ranges summed over sequences and heads
-// and `target` the workgroups the chip holds at once, C is W / target: about
-// one unit for each of them, or one per tile where there are many tiles. The
-// row kernels refine that:
-//   - the last part of a tile is short, so there are more units than
-//     W / C: C is raised until they fit one round (32 sequences of up to 8192
-//     positions x 8 heads: 640 units in 512 places took 139 us, 512 in 128);
-//   - with much work per unit, or more tiles than half the places, several
-//     rounds of smaller parts even out better (2048 units: 121 us);
-//   - short parts are not worth a join: up to 512 positions per part as long
-//     as a tile has no more than 16 parts and half the places are taken (one
-//     token over 131072 positions: 256 parts 20.5 us, 512 parts 24).
+// and `target` the workgroups the chip holds at once, C starts as W / target:
+//   - the last part of a tile is short, so that gives more units than W / C: C
+//     is raised until they fit one round (32 sequences of up to 8192 positions
+//     x 8 heads: 640 units in 512 places took 139 us, 512 in 128);
+//   - row kernels, with much work per unit or more tiles than half the places:
+//     several rounds of smaller parts even out better (2048 units: 121 us);
+//   - row kernels: short parts are not worth a join: up to 512 positions per
+//     part as long as a tile has no more than 16 parts and half the places are
+//     taken (one token over 131072 positions: 256 parts 20.5 us, 512 parts 24);
+//   - tile kernels, with more tiles than half the places: the join of 128 rows
+//     costs more than an uneven round, so C is twice that (440 tiles: 288 us,
+//     cut for 512 places 446; 256 tiles cut in two: 177 us, whole 203).
 template <int ROWS>
 struct Partition {
     struct Shape {
@@ -180,23 +181,23 @@ struct Partition {
         // Rounded up past the error of FP32: a larger c only means fewer parts.
         const float all = ((float)(unsigned)last_lane((int)(w >> 32)) * 0x1p32f + (float)(unsigned)last_lane((int)w)) *
                           (float)a.kv_heads * 1.00001f;
-        float per = all * a.per_target;
+        const float per = all * a.per_target;
+        const float tiles = (float)last_lane(wave_scan(t)) * (float)a.kv_heads;
+        bool fit = tiles <= 0.5f * (float)a.target;
         if (ROWS <= 32) {
-            const float tiles = (float)last_lane(wave_scan(t)) * (float)a.kv_heads;
-            const bool even = per < 2048.f && tiles <= 0.5f * (float)a.target;
-            if (!even)
-                per /= (float)a.rounds;
-            set_part(fmaxf(per, fminf(512.f, fmaxf((float)wave_max(longest) * (1.f / 16), all * a.per_target * 2.f))));
-            if (even && a.seqs <= kWave)
-                for (int i = 0; i < 2; ++i) {
-                    const int n = last_lane(wave_scan(units()));
-                    if (n <= a.target)
-                        break;
-                    set_part((float)c * (float)n * a.per_target);
-                }
+            fit = fit && per < 2048.f;
+            set_part(fmaxf(fit ? per : per / (float)a.rounds,
+                           fminf(512.f, fmaxf((float)wave_max(longest) * (1.f / 16), all * a.per_target * 2.f))));
         } else {
-            set_part(per);
+            set_part(fit ? per : 2.f * per);
         }
+        if (fit && a.seqs <= kWave)
+            for (int i = 0; i < 2; ++i) {
+                const int n = last_lane(wave_scan(units()));
+                if (n <= a.target)
+                    break;
+                set_part((float)c * (float)n * a.per_target);
+            }
     }
     __device__ void set_part(float positions)
     {
@@ -207,8 +208,12 @@ struct Partition {
     }
     __device__ int units() const { return s.tiles * s.splits * a.kv_heads; }
     __device__ int slots() const { return s.splits > 1 ? units() : 0; }
-    // Rows whose splits have to be joined.
-    __device__ int joins() const { return s.splits > 1 ? s.n * a.group * a.kv_heads : 0; }
+    // Blocks of rows whose splits have to be joined (join_rows each, attn_join.h).
+    __device__ int joins(int few, int rows) const
+    {
+        const int per = s.splits <= few ? rows : 1;
+        return s.splits > 1 ? (s.n * a.group + per - 1) / per * a.kv_heads : 0;
+    }
 
     template <class Count>
     __device__ int total(Count count)
@@ -344,9 +349,9 @@ __device__ __forceinline__ void write_lse(const AttnArgs &a, int tok, int head, 
             l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * 0.693147181f : -INFINITY;
 }
 
-// Slots of the workspace, accessed past the XCD-local L2: they are exchanged
-// between workgroups.
-template <int DIM, int ROWS>
+// Slots of the workspace. SCOPE kDeviceScope passes the XCD-local L2, for
+// splits joined in the launch that made them; 0 is enough across launches.
+template <int DIM, int ROWS, int SCOPE>
 struct Slots {
     static constexpr uint32_t kSlot = ROWS * (DIM + 2) * 4u;
     static constexpr uint32_t kStats = ROWS * DIM * 4u;
@@ -360,12 +365,11 @@ struct Slots {
     __device__ __forceinline__ void put(int slot, int r, int d, f32x4 v, float m, float l) const
     {
         const uint32_t at = (uint32_t)slot * kSlot;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ws, at + (uint32_t)(r * DIM + d) * 4u, 0,
-                                               kDeviceScope);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ws, at + (uint32_t)(r * DIM + d) * 4u, 0, SCOPE);
         if (d == 0)
             __builtin_amdgcn_raw_buffer_store_b64(
                 u32x2{__builtin_bit_cast(uint32_t, m), __builtin_bit_cast(uint32_t, l)}, ws,
-                at + kStats + (uint32_t)r * 8u, 0, kDeviceScope);
+                at + kStats + (uint32_t)r * 8u, 0, SCOPE);
     }
     // Joins slots first, first + stride, .. of one row's elements d .. d + 3:
     // `members` of them, at most N, all loads in flight, in order.
@@ -379,8 +383,8 @@ struct Slots {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const uint32_t at = i < members ? (uint32_t)(first + i * stride) * kSlot : kEnd;
-            st[i] = __builtin_amdgcn_raw_buffer_load_b64(ws, at + kStats + (uint32_t)r * 8u, 0, kDeviceScope);
-            v[i] = __builtin_amdgcn_raw_buffer_load_b128(ws, at + (uint32_t)(r * DIM + d) * 4u, 0, kDeviceScope);
+            st[i] = __builtin_amdgcn_raw_buffer_load_b64(ws, at + kStats + (uint32_t)r * 8u, 0, SCOPE);
+            v[i] = __builtin_amdgcn_raw_buffer_load_b128(ws, at + (uint32_t)(r * DIM + d) * 4u, 0, SCOPE);
         }
         // (m and l by value: a bit cast of a vector's element takes element 0)
         float m[N];
@@ -405,13 +409,14 @@ struct Slots {
     }
 };
 
-constexpr int kTilePos = 64;               // positions of the tile kernel's tiles
+// Positions of the tile kernel's tiles.
+constexpr int attn_tile_pos(int dim) { return dim == 256 ? 32 : 64; }
 
 using AttnKernel = void (*)(AttnArgs);
 // Row kernels for tiles of 16 * nb rows (nb 1, 2); nullptr if not built.
 AttnKernel attn_rows_kernel(int dtype, int dim, int nb);
-// Tile kernels for tiles of 32 * waves rows (waves 2, 4), 64 * waves threads.
-AttnKernel attn_tile_kernel(int dtype, int dim, int waves);
+// Tile kernels for tiles of 64 or 128 rows, two threads per row.
+AttnKernel attn_tile_kernel(int dtype, int dim, int rows);
 // Join kernels for tiles of 16, 32, 64 or 128 rows, kJoinThreads threads.
 AttnKernel attn_join_kernel(int dtype, int dim, int rows);
 constexpr int kJoinThreads = 256;

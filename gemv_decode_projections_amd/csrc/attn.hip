@@ -310,14 +310,14 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
         a.rounds = 4 / nb;
         fn = reinterpret_cast<const void *>(attn_rows_kernel(cache->dtype, cache->head_dim, nb));
     } else {
-        const int waves = seq_rows <= 64 ? 2 : 4;
-        tile = 32 * waves;
-        threads = 64 * waves;
-        a.kv_step = kTilePos;
-        a.min_split = 4 * kTilePos;
-        // Splits of 128 rows cost more than an uneven round.
-        a.target = waves == 2 ? 512 : 256;
-        fn = reinterpret_cast<const void *>(attn_tile_kernel(cache->dtype, cache->head_dim, waves));
+        tile = seq_rows <= 64 ? 64 : 128;
+        threads = 2 * tile;
+        a.kv_step = 64;
+        a.min_split = 256;
+        // Two workgroups per compute unit; one where a head's 256 elements
+        // take all registers.
+        a.target = cache->head_dim == 256 ? 256 : 512;
+        fn = reinterpret_cast<const void *>(attn_tile_kernel(cache->dtype, cache->head_dim, tile));
     }
     if (tile > 16)
         join = reinterpret_cast<const void *>(attn_join_kernel(cache->dtype, cache->head_dim, tile));

@@ -6,12 +6,12 @@
 
 namespace gdp {
 
-// Joins the splits of a tile kernel's rows, one row per workgroup and pass:
-// threads in groups of DIM / 4, group g takes kJoinRun consecutive splits of
-// every kJoinThreads / (DIM / 4) * kJoinRun, each thread four elements; the
-// groups' results meet in LDS, in order. Splits of 64 to 128 rows are too much
-// for one workgroup per tile: joined in the tile kernel by the last of 16
-// workgroups they cost 30 us a level.
+// Threads in groups of DIM / 4, each thread four elements of a row. Where a
+// tile has at most kJoinRun splits a group joins a row by itself; with more, a
+// workgroup joins one row: group g takes kJoinRun consecutive splits of every
+// GROUPS * kJoinRun, and the groups' results meet in LDS, in order. (Joined in
+// the tile kernel by the last of 16 workgroups, splits of 64 rows cost 30 us a
+// level.)
 constexpr int kJoinRun = 8;
 
 template <class T, int DIM, int ROWS>
@@ -22,36 +22,47 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join(AttnArgs a)
     __shared__ f32x4 s_o[GROUPS][PER];
     __shared__ float s_m[GROUPS], s_l[GROUPS];
     Partition<ROWS> part(a);
-    auto joins = [](const Partition<ROWS> &p) { return p.joins(); };
+    auto joins = [](const Partition<ROWS> &p) { return p.joins(kJoinRun, GROUPS); };
     const int total = part.total(joins);
-    const Slots<DIM, ROWS> slots(a);
-    const int g = threadIdx.x / PER, lane = threadIdx.x % PER;
+    const Slots<DIM, ROWS, 0> slots(a);
+    const int g = threadIdx.x / PER, d = 4 * (threadIdx.x % PER);
     for (int id = blockIdx.x; id < total; id += gridDim.x) {
         AttnUnit u;
         int tiles;
         const int local = part.find(id, joins, u, tiles);
-        const int rows = u.n * a.group;
-        u.kvh = local / rows;
-        const int row = local - u.kvh * rows;
-        const int tile = row / ROWS;
+        const bool few = u.splits <= kJoinRun;
+        const int rows = u.n * a.group, per = few ? GROUPS : 1, blocks = (rows + per - 1) / per;
+        u.kvh = local / blocks;
+        const int row = (local - u.kvh * blocks) * per + (few ? g : 0);
+        if (few && row >= rows)
+            continue;
+        const int tile = row / ROWS, r = row % ROWS;
         const int first = u.slot0 + (u.kvh * tiles + tile) * u.splits;
         int tok, head;
         row_place(a, u, row, tok, head);
-        const u32x2 gate = a.gate ? load_gate(a, tok, head, 4 * lane) : u32x2{0, 0};
-        float top = -INFINITY, sum = 0.f;
+        const u32x2 gate = a.gate && (few || g == 0) ? load_gate(a, tok, head, d) : u32x2{0, 0};
+        float top, sum;
+        if (few) {
+            const f32x4 v = slots.template join<kJoinRun>(first, 1, u.splits, r, d, top, sum);
+            write_out<T>(a, tok, head, d, v, sum, gate);
+            if (d == 0)
+                write_lse(a, tok, head, top, sum);
+            continue;
+        }
+        top = -INFINITY;
+        sum = 0.f;
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
         for (int s = g * kJoinRun; s < u.splits; s += GROUPS * kJoinRun) {
             float m, l;
-            const f32x4 v = slots.template join<kJoinRun>(first + s, 1, min(kJoinRun, u.splits - s), row - tile * ROWS,
-                                                          4 * lane, m, l);
+            const f32x4 v = slots.template join<kJoinRun>(first + s, 1, min(kJoinRun, u.splits - s), r, d, m, l);
             const float big = fmaxf(top, m), safe = big == -INFINITY ? 0.f : big;
             const float f = exp2_fast(top - safe), h = exp2_fast(m - safe);
             acc = acc * f + v * h;
             sum = sum * f + l * h;
             top = big;
         }
-        s_o[g][lane] = acc;
-        if (lane == 0) {
+        s_o[g][d / 4] = acc;
+        if (d == 0) {
             s_m[g] = top;
             s_l[g] = sum;
         }
@@ -65,11 +76,11 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join(AttnArgs a)
             sum = 0.f;
             for (int i = 0; i < used; ++i) {
                 const float f = exp2_fast(s_m[i] - safe);
-                acc += s_o[i][lane] * f;
+                acc += s_o[i][d / 4] * f;
                 sum += s_l[i] * f;
             }
-            write_out<T>(a, tok, head, 4 * lane, acc, sum, gate);
-            if (lane == 0)
+            write_out<T>(a, tok, head, d, acc, sum, gate);
+            if (d == 0)
                 write_lse(a, tok, head, top, sum);
         }
         __syncthreads();

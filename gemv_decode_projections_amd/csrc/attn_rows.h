@@ -345,7 +345,7 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
         if (d == 0)
             write_lse(a, tok, head, m, l);
     };
-    const Slots<DIM, ROWS> slots(a);
+    const Slots<DIM, ROWS, NB == 1 ? kDeviceScope : 0> slots(a);
 #pragma unroll 1
     for (int r = r0; r < u.nrows; r += RSTEP) {
         float m = s_m[0][r];

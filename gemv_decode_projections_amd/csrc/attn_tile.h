@@ -2,7 +2,8 @@
 // prompt) over a paged cache: keys and values go through LDS once for all the
 // rows of a workgroup.
 //
-// Mathematics, per wave of 32 rows and tile of 64 positions, on v_mfma
+// Mathematics, per block of 32 rows and tile of 64 positions (32 for heads of
+// 256 elements, whose accumulators leave fewer registers), on v_mfma
 // 32x32x16 (A: lane l holds row l%32, k = 8 (l/32) + 0..7; B: column l%32, the
 // same k; C: column l%32, rows 8 (i/4) + 4 (l/32) + i%4 for i = 0..15):
 //   S^T (64 x 32) = K Q^T         A = keys from LDS, B = queries in registers;
@@ -21,6 +22,8 @@
 // tile row's 16-byte pieces are permuted (by the address that each lane of the
 // DMA reads) so that neither read meets a bank conflict.
 #pragma once
+
+#include <type_traits>
 
 #include "attn.h"
 
@@ -54,18 +57,24 @@ __device__ __forceinline__ void wait_vm()
 }
 
 template <class T, int DIM, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void attn_tile(AttnArgs a)
+__global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void attn_tile(AttnArgs a)
 {
     constexpr int ROWS = 32 * WAVES;
     constexpr int KS = DIM / 16;                     // k-steps of Q K^T
     constexpr int DB = DIM / 32;                     // 32-element blocks of the output
     constexpr int ROWB = DIM * 2;
-    constexpr int TILEB = kTilePos * ROWB;           // bytes of one tile of K or V
+    constexpr int POS = attn_tile_pos(DIM);          // positions of a tile
+    constexpr int HALVES = POS / 32;
+    constexpr int TILEB = POS * ROWB;                // bytes of one tile of K or V
     constexpr int RPI = 1024 / ROWB;                 // rows per DMA instruction (8, 4 or 2)
-    constexpr int NI = kTilePos / RPI / WAVES;       // DMA instructions per wave and tile, each of K and V
-    constexpr int STAGES = 2;
+    constexpr int NI = POS / RPI / WAVES;       // DMA instructions per wave and tile, of K as of V
     constexpr float RAISE = 8.0f;
-    __shared__ __align__(1024) char s_ring[STAGES][2][TILEB];
+    // The ring of tiles; at the end each wave's 32 rows in FP32, 16-byte pieces
+    // permuted so that neither side meets a bank conflict.
+    constexpr int OUTB = ROWS * DIM * 4;
+    __shared__ __align__(1024) char s_mem[4 * TILEB > OUTB ? 4 * TILEB : OUTB];
+    char(&s_k)[2][TILEB] = *reinterpret_cast<char(*)[2][TILEB]>(s_mem);
+    char(&s_v)[2][TILEB] = *reinterpret_cast<char(*)[2][TILEB]>(s_mem + 2 * TILEB);
 
     AttnUnit u;
     if (!find_unit<ROWS>(a, blockIdx.x, u))
@@ -107,18 +116,32 @@ __global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void 
     // lane l row RPI n + l / (64 / RPI), piece l % (64 / RPI) of LDS.
     constexpr int PIECES = 64 / RPI;
     const int sub = lane / PIECES, piece = lane % PIECES;
-    auto issue = [&](int base, int stage) {
-        const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)&s_ring[stage][0][0];
+    const uint32_t sub_off = (uint32_t)sub * (uint32_t)a.token_stride;
+    auto lds_of = [](char *p) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)p; };
+    // (the pages of a tile are read one tile before its DMA)
+    int pages[NI];
+    auto read_pages = [&](int base) {
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+            pages[n] = page_of(base + (wave * NI + n) * RPI);
+    };
+    auto issue = [&](int base, auto stage) {
+        int64_t off[NI];
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+            kv_offset(a, pages[n], base + (wave * NI + n) * RPI, head_off, off[n]);
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
             const int row = (wave * NI + n) * RPI;
-            int64_t off;
-            kv_offset(a, page_of(base + row), base + row, head_off, off);
-            const uint32_t step = (uint32_t)sub * (uint32_t)a.token_stride;
-            dma_rows(a.k + off, step + 16 * key_piece<DIM>(row + sub, piece), lds + row * ROWB);
-            dma_rows(a.v + off, step + 16 * value_piece<DIM>(row + sub, piece), lds + TILEB + row * ROWB);
+            dma_rows(a.k + off[n], sub_off + 16 * key_piece<DIM>(row + sub, piece), lds_of(s_k[stage.value]) + row * ROWB);
+        }
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const int row = (wave * NI + n) * RPI;
+            dma_rows(a.v + off[n], sub_off + 16 * value_piece<DIM>(row + sub, piece), lds_of(s_v[stage.value]) + row * ROWB);
         }
     };
+    auto barrier = [] { asm volatile("s_barrier" ::: "memory"); };
 
     f32x16 acc[DB];
 #pragma unroll
@@ -126,10 +149,9 @@ __global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void 
         acc[d] = f32x16{};
     float top = -INFINITY, sum = 0.f;
 
-    // Value fragment of positions 32 pb + 16 s + 4 half + {0..3, 8..11},
-    // element 32 d + col, by two transposing reads: of each 16 lanes, lane i
-    // points at row i / 4, elements 4 (i % 4) .. + 3, and receives element i
-    // of the four rows.
+    // Value fragment of positions k0 + 4 half + {0..3, 8..11}, element 32 d +
+    // col, by two transposing reads: of each 16 lanes, lane i points at row
+    // i / 4, elements 4 (i % 4) .. + 3, and receives element i of the four rows.
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     const int trow = 4 * half + lane % 16 / 4;
     const int tcol = 16 * (lane / 16 % 2) + 4 * (lane % 4);
@@ -139,66 +161,55 @@ __global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void 
         for (int p = 0; p < 2; ++p) {
             const int row = k0 + 8 * p + trow, el = 32 * d + tcol;
             const char *at = v + row * ROWB + 16 * value_piece<DIM>(row, el / 8) + el % 8 * 2;
-            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4 *)at);
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
             const u32x2 y = __builtin_bit_cast(u32x2, x);
             f[2 * p] = y.x;
             f[2 * p + 1] = y.y;
         }
         return f;
     };
-
-    if (u.lo < u.hi)
-        issue(u.lo, 0);
-    int stage = 0;
-    for (int base = u.lo; base < u.hi; base += kTilePos, stage ^= 1) {
-        wait_vm<0>();
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (base + kTilePos < u.hi)
-            issue(base + kTilePos, stage ^ 1);
-        const char *kt = s_ring[stage][0], *vt = s_ring[stage][1];
-
-        f32x16 s[2];
+    // Scores of a tile's halves, their chains of products side by side.
+    auto scores = [&](const char *k, f32x16 (&s)[HALVES]) {
 #pragma unroll
-        for (int pb = 0; pb < 2; ++pb) {
-            s[pb] = f32x16{};
+        for (int h = 0; h < HALVES; ++h)
+            s[h] = f32x16{};
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const int row = 32 * pb + col;
-                const u32x4 kf =
-                    *reinterpret_cast<const u32x4 *>(kt + row * ROWB + 16 * key_piece<DIM>(row, 2 * ks + half));
-                s[pb] = T::mfma32(kf, qf[ks], s[pb]);
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                const int row = 32 * h + col;
+                s[h] = T::mfma32(
+                    *reinterpret_cast<const u32x4 *>(k + row * ROWB + 16 * key_piece<DIM>(row, 2 * ks + half)), qf[ks],
+                    s[h]);
+            }
+    };
+    auto needs_mask = [&](int p) { return holes || p < all_lo || p + POS > all_hi || p + POS > u.hi; };
+    // Masks the scores of positions p .. p + 31; bit i of the result: position
+    // p + 8 (i / 4) + 4 half + i % 4 holds a token.
+    auto mask = [&](int p, f32x16 &s) {
+        uint32_t held = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int p0 = p + 8 * g + 4 * half;
+            const bool ok = !holes || (unsigned)a.table[(int64_t)u.seq * a.table_stride +
+                                                        min(p0 >> a.page_shift, a.table_width - 1)] < (unsigned)a.n_pages;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = ok && p0 + e < u.hi;
+                held |= in ? 1u << (4 * g + e) : 0u;
+                if (!(in && p0 + e >= see_lo && p0 + e < see_hi))
+                    s[4 * g + e] = -INFINITY;
             }
         }
-        const bool masked = holes || base < all_lo || base + kTilePos > all_hi || base + kTilePos > u.hi;
-        uint32_t held = 0xffffffffu;       // bit 16 pb + i: position 32 pb + 8 (i / 4) + 4 half + i % 4
-        if (masked) {
+        return held;
+    };
+    // Raises the rows' maxima to fit the scores, rescaling what was summed.
+    auto raise = [&](const f32x16 (&s)[HALVES]) {
+        // (the maximum that passes NaN on: it needs no canonical operands)
+        float m = s[0][0];
 #pragma unroll
-            for (int pb = 0; pb < 2; ++pb)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int p0 = base + 32 * pb + 8 * g + 4 * half;
-                    const bool ok = !holes || (unsigned)a.table[(int64_t)u.seq * a.table_stride +
-                                                                min(p0 >> a.page_shift, a.table_width - 1)] <
-                                                  (unsigned)a.n_pages;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int p = p0 + e;
-                        const bool in = ok && p < u.hi;
-                        if (!in)
-                            held &= ~(1u << (16 * pb + 4 * g + e));
-                        if (!(in && p >= see_lo && p < see_hi))
-                            s[pb][4 * g + e] = -INFINITY;
-                    }
-                }
-        }
-        float m = -INFINITY;
-#pragma unroll
-        for (int pb = 0; pb < 2; ++pb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                m = fmaxf(m, s[pb][i]);
+        for (int i = 1; i < 16 * HALVES; ++i)
+            m = __builtin_elementwise_maximum(m, s[i / 16][i % 16]);
         m = max32(m) * a.scale_log2;
         if (__any(m > top + RAISE)) {
             const float raised = fmaxf(m, top);
@@ -209,104 +220,173 @@ __global__ __launch_bounds__(64 * WAVES, DIM == 256 || WAVES == 2 ? 1 : 2) void 
             for (int d = 0; d < DB; ++d)
                 acc[d] *= f;
         }
+    };
+    // Probabilities in 16 bits for the matrix instruction: each within half a
+    // unit of the type, errors that average out over a row; the sum keeps the
+    // unrounded ones.
+    auto weights = [&](const f32x16 &s, u32x4 (&pf)[2]) {
         const float safe = top == -INFINITY ? 0.f : top;
-        // Probabilities in 16 bits for the matrix instruction: each within
-        // half a unit of the type, errors that average out over a row; the sum
-        // keeps the unrounded ones.
-        u32x4 pf[2][2];
 #pragma unroll
-        for (int pb = 0; pb < 2; ++pb)
+        for (int i = 0; i < 16; i += 2) {
+            const float p0 = exp2_fast(__builtin_fmaf(s[i], a.scale_log2, -safe));
+            const float p1 = exp2_fast(__builtin_fmaf(s[i + 1], a.scale_log2, -safe));
+            sum += p0;
+            sum += p1;
+            pf[i / 8][i % 8 / 2] = T::pack(p0, p1);
+        }
+    };
+    auto product = [&](const char *v, int h, const u32x4 (&pf)[2]) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const float p0 = exp2_fast(__builtin_fmaf(s[pb][i], a.scale_log2, -safe));
-                const float p1 = exp2_fast(__builtin_fmaf(s[pb][i + 1], a.scale_log2, -safe));
-                sum += p0;
-                sum += p1;
-                pf[pb][i / 8][i % 8 / 2] = T::pack(p0, p1);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                acc[d] = T::mfma32(value_frag(v, 32 * h + 16 * t, d), pf[t], acc[d]);
+    };
+    // The same for half a tile with masked positions p .. p + 31. Values past
+    // the last token or on unmapped pages are not the cache's: zero. One that
+    // only some rows see may be an infinity or a NaN, which a zero weight does
+    // not silence in a product: it is left out of the product and added to the
+    // rows that see it.
+    auto masked_product = [&](const char *v, int h, int p, uint32_t held, const u32x4 (&pf)[2]) {
+        bool poisoned = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            u32x4 keep;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t bits = held >> (8 * t + 2 * e);
+                keep[e] = (bits & 1 ? 0xffffu : 0u) | (bits & 2 ? 0xffff0000u : 0u);
             }
-        if (!masked) {
 #pragma unroll
-            for (int pb = 0; pb < 2; ++pb)
+            for (int d = 0; d < DB; ++d) {
+                u32x4 f = value_frag(v, 32 * h + 16 * t, d) & keep;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        acc[d] = T::mfma32(value_frag(vt, 32 * pb + 16 * t, d), pf[pb][t], acc[d]);
-        } else {
-            // Values past the last token or on unmapped pages are not the
-            // cache's: zero. One that only some rows see may be an infinity or
-            // a NaN, which a zero weight does not silence in a product: it is
-            // left out of the product and added to the rows that see it.
-            bool poisoned = false;
-#pragma unroll
-            for (int pb = 0; pb < 2; ++pb)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    u32x4 keep;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t b = held >> (16 * pb + 8 * t + 2 * e);
-                        keep[e] = (b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u);
-                    }
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        u32x4 f = value_frag(vt, 32 * pb + 16 * t, d) & keep;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            poisoned |= not_finite<T>(f[e]);
-                            f[e] = finite_only<T>(f[e]);
-                        }
-                        acc[d] = T::mfma32(f, pf[pb][t], acc[d]);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    poisoned |= not_finite<T>(f[e]);
+                    f[e] = finite_only<T>(f[e]);
                 }
-            if (__any(poisoned))
-                for (int pos = 0; pos < kTilePos; ++pos) {
-                    if (base + pos >= u.hi || (unsigned)page_of(base + pos) >= (unsigned)a.n_pages)
-                        continue;
-                    const int i = pos % 32 / 8 * 4 + pos % 4;
-                    uint32_t pair = 0;
+                acc[d] = T::mfma32(f, pf[t], acc[d]);
+            }
+        }
+        if (!__any(poisoned))
+            return;
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j) {
+            if (p + j >= u.hi || (unsigned)page_of(p + j) >= (unsigned)a.n_pages)
+                continue;
+            const int i = j / 8 * 4 + j % 4;
+            uint32_t pair = 0;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (k == pos / 32 * 8 + i / 2)
-                            pair = pf[k / 8][k / 4 % 2][k % 4];
-                    const float w = __shfl(i % 2 ? T::hi(pair) : T::lo(pair), pos / 4 % 2 * 32 + col);
-                    if (base + pos < see_lo || base + pos >= see_hi)
-                        continue;
+            for (int k = 0; k < 8; ++k)
+                if (k == i / 2)
+                    pair = pf[k / 4][k % 4];
+            const float w = __shfl(i % 2 ? T::hi(pair) : T::lo(pair), j / 4 % 2 * 32 + col);
+            if (p + j < see_lo || p + j >= see_hi)
+                continue;
 #pragma unroll
-                    for (int d = 0; d < DB; ++d)
+            for (int d = 0; d < DB; ++d)
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int el = 32 * d + 8 * g + 4 * half;
-                            const u32x2 x = *reinterpret_cast<const u32x2 *>(
-                                vt + pos * ROWB + 16 * value_piece<DIM>(pos, el / 8) + el % 8 * 2);
-                            const float v[4] = {T::lo(x.x), T::hi(x.x), T::lo(x.y), T::hi(x.y)};
+                for (int g = 0; g < 4; ++g) {
+                    const int el = 32 * d + 8 * g + 4 * half;
+                    const u32x2 x = *reinterpret_cast<const u32x2 *>(
+                        v + (32 * h + j) * ROWB + 16 * value_piece<DIM>(32 * h + j, el / 8) + el % 8 * 2);
+                    const float val[4] = {T::lo(x.x), T::hi(x.x), T::lo(x.y), T::hi(x.y)};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (!__builtin_isfinite(v[e]))
-                                    acc[d][4 * g + e] += w * v[e];
-                        }
+                    for (int e = 0; e < 4; ++e)
+                        if (!__builtin_isfinite(val[e]))
+                            acc[d][4 * g + e] += w * val[e];
                 }
         }
+    };
+    // The queries are here before the first DMA: a wait for them inside the loop
+    // would wait for the DMA issued behind them.
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+        asm volatile("" : "+v"(qf[ks]));
+
+    // One tile: its K and V are waited for, the next one's set off. Tiles that
+    // need masks have a loop of their own, which keeps the other one lean.
+    typedef std::integral_constant<int, 0> Stage0;
+    typedef std::integral_constant<int, 1> Stage1;
+    auto step = [&](int base, auto stage, auto other, auto masked) {
+        wait_vm<0>();
+        barrier();
+        if (base + POS < u.hi) {
+            issue(base + POS, other);
+            read_pages(base + 2 * POS);
+        }
+        const char *k = s_k[stage.value], *v = s_v[stage.value];
+        f32x16 s[HALVES];
+        scores(k, s);
+        uint32_t held[HALVES];
+        if constexpr (masked.value)
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+                held[h] = mask(base + 32 * h, s[h]);
+        raise(s);
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+            u32x4 pf[2];
+            weights(s[h], pf);
+            if constexpr (masked.value)
+                masked_product(v, h, base + 32 * h, held[h], pf);
+            else
+                product(v, h, pf);
+        }
+    };
+    if (u.lo < u.hi) {
+        read_pages(u.lo);
+        issue(u.lo, Stage0());
+        read_pages(u.lo + POS);
     }
-    sum = sum32(sum);
-    // Out of the unit: straight to the output if the tile has one split, else
-    // to the unit's slot for the join kernel.
-    if (r >= u.nrows)
-        return;
-    const Slots<DIM, ROWS> slots(a);
+    // (in pairs, so that a tile's place in LDS is a constant)
+    for (int base = u.lo; base < u.hi;) {
+#pragma unroll 1
+        for (; base < u.hi && (needs_mask(base) || needs_mask(base + POS)); base += 2 * POS) {
+            step(base, Stage0(), Stage1(), std::true_type());
+            if (base + POS < u.hi)
+                step(base + POS, Stage1(), Stage0(), std::true_type());
+        }
+#pragma unroll 1
+        for (; base < u.hi && !(needs_mask(base) || needs_mask(base + POS)); base += 2 * POS) {
+            step(base, Stage0(), Stage1(), std::false_type());
+            step(base + POS, Stage1(), Stage0(), std::false_type());
+        }
+    }
+    // Out of the unit, through LDS, so that a row is written whole: straight
+    // to the output if the tile has one split, else to the unit's slot for the
+    // join kernel.
+    __syncthreads();
+    constexpr int PIECES_O = DIM / 4;                // 16-byte pieces of a row
+    char *rows = s_mem + wave * 32 * DIM * 4;
+    auto place = [](int row, int p) { return (row * PIECES_O + (p ^ (row % 16))) * 16; };
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int el = 32 * d + 8 * g + 4 * half;
-            const f32x4 v = {acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
-            if (u.splits == 1)
-                write_out<T>(a, tok, head, el, v, sum, a.gate ? load_gate(a, tok, head, el) : u32x2{0, 0});
-            else
-                slots.put(u.slot0 + u.split, r, el, v, top, sum);
-        }
-    if (u.splits == 1 && half == 0)
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<f32x4 *>(rows + place(col, 8 * d + 2 * g + half)) =
+                f32x4{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
+    sum = sum32(sum);
+    if (u.splits == 1 && half == 0 && r < u.nrows)
         write_lse(a, tok, head, top, sum);
+    const Slots<DIM, ROWS, 0> slots(a);
+    constexpr int PER_PASS = 64 / PIECES_O < 1 ? 1 : 64 / PIECES_O;
+    const int p = lane % PIECES_O;
+#pragma unroll 4
+    for (int i = 0; i < 32; i += PER_PASS) {
+        const int row = i + lane / PIECES_O;
+        const float m = __shfl(top, row), l = __shfl(sum, row);
+        if (wave * 32 + row >= u.nrows)
+            continue;
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(rows + place(row, p));
+        if (u.splits == 1) {
+            int t, h;
+            row_place(a, u, u.row0 + wave * 32 + row, t, h);
+            write_out<T>(a, t, h, 4 * p, v, l, a.gate ? load_gate(a, t, h, 4 * p) : u32x2{0, 0});
+        } else {
+            slots.put(u.slot0 + u.split, wave * 32 + row, 4 * p, v, m, l);
+        }
+    }
 }
 
 }  // namespace gdp
