@@ -7,19 +7,26 @@ projections of a decode block.
 
 Argument marshalling and checks only, as in `binding`: the work runs in the HIP
 library, on the stream given or torch's current one. Calls launch and return;
-nothing is allocated, synchronized or copied to the host.
+nothing is allocated, synchronized or copied to the host. The run functions'
+checks are compiled (csrc/block_py.cpp): a tensor of the wrong shape, type,
+device or layout raises ValueError before anything is launched, what the
+library itself refuses raises ProjError.
 """
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
 from . import binding as _b
 
-_i, _i64, _vp, _f = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+_i, _i64, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 HEAD_DIMS = (64, 128, 256)
+EXT_PATH = os.path.join(os.path.dirname(_b.LIB_PATH), "_block.so")
 
 
 class _Cache(ctypes.Structure):
@@ -27,58 +34,49 @@ class _Cache(ctypes.Structure):
                 ("n_pages", _i), ("page_size", _i), ("kv_heads", _i), ("head_dim", _i), ("dtype", _i)]
 
 
-class _Batch(ctypes.Structure):
-    _fields_ = [("q_start", _vp), ("kv_len", _vp), ("table", _vp), ("table_stride", _i64), ("table_width", _i),
-                ("seqs", _i), ("tokens", _i)]
-
-
-class _Attn(ctypes.Structure):
-    _fields_ = [("q", _vp), ("gate", _vp), ("out", _vp), ("lse", _vp), ("q_stride", _i64), ("q_head_stride", _i64),
-                ("gate_stride", _i64), ("gate_head_stride", _i64), ("out_stride", _i64), ("out_head_stride", _i64),
-                ("heads", _i), ("max_q", _i), ("window", _i), ("scale", _f)]
-
-
 class _W4(ctypes.Structure):
     _fields_ = [("n", _i), ("k", _i), ("group", _i), ("dtype", _i), ("has_zeros", _i)]
 
 
-class _Norm(ctypes.Structure):
-    _fields_ = [("x", _vp), ("residual", _vp), ("gate", _vp), ("weight_post", _vp), ("weight_pre", _vp),
-                ("residual_out", _vp), ("out", _vp), ("x_stride", _i64), ("residual_stride", _i64),
-                ("gate_stride", _i64), ("residual_out_stride", _i64), ("out_stride", _i64), ("width", _i),
-                ("dtype", _i), ("residual_dtype", _i), ("alpha", _f), ("eps", _f)]
-
-
-_FUNCS = None
+_LIB = None
+_EXT = None
 
 
 def _lib():
-    """The library with block.h's signatures set."""
-    global _FUNCS
-    if _FUNCS is None:
+    """The library with the signatures of block.h's other functions set."""
+    global _LIB
+    if _LIB is None:
         lib = _b._lib()
-        cache, batch = ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
+        shape = ctypes.POINTER(_W4)
         sig = {
-            "blk_kv_append": ([cache, batch, _vp, _vp, _i64, _i64, _vp], _i),
-            "blk_kv_copy_pages": ([cache, _vp, _vp, _i, _vp], _i),
-            "blk_attn_run": ([cache, batch, ctypes.POINTER(_Attn), _vp, ctypes.c_size_t, _vp], _i),
             "blk_attn_workspace_bytes": ([_i], ctypes.c_size_t),
-            "blk_w4_packed_bytes": ([ctypes.POINTER(_W4)], ctypes.c_size_t),
-            "blk_w4_pack": ([ctypes.POINTER(_W4), _vp, _vp, _vp, _vp, _vp], _i),
-            "blk_w4_run": ([ctypes.POINTER(_W4), _vp, _vp, _i64, _i, _vp, _i64, _vp], _i),
-            "blk_norm_run": ([ctypes.POINTER(_Norm), _i, _vp], _i),
+            "blk_w4_packed_bytes": ([shape], ctypes.c_size_t),
+            "blk_w4_pack": ([shape, _vp, _vp, _vp, _vp, _vp], _i),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = res
-        _FUNCS = lib
-    return _FUNCS
+        _LIB = lib
+    return _LIB
 
 
-def _raw_stream(stream, device):
+def _ext():
+    """The compiled run functions."""
+    global _EXT
+    if _EXT is None:
+        _lib()
+        if not os.path.exists(EXT_PATH):
+            raise RuntimeError("%s is not built; run `python -m gemv_decode_projections_amd.build` first" % EXT_PATH)
+        loader = importlib.machinery.ExtensionFileLoader("_block", EXT_PATH)
+        _EXT = importlib.util.module_from_spec(importlib.util.spec_from_loader("_block", loader))
+        loader.exec_module(_EXT)
+    return _EXT
+
+
+def _raw_stream(stream, index):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -113,7 +111,7 @@ class KvCache:
         self.dtype, self.device = k.dtype, k.device
         s = k.stride()
         self._c = _Cache(k.data_ptr(), v.data_ptr(), s[0], s[1], s[2], pages, size, heads, dim, DTYPES[k.dtype])
-        self._ref = ctypes.byref(self._c)
+        self._addr, self._index = ctypes.addressof(self._c), k.device.index
 
     @classmethod
     def empty(cls, n_pages, page_size, kv_heads, head_dim, dtype=torch.bfloat16, device="cuda"):
@@ -122,55 +120,22 @@ class KvCache:
         return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
 
 
-def _batch(cache, table, q_start, kv_len, tokens):
-    for what, t, dims in (("table", table, 2), ("q_start", q_start, 1), ("kv_len", kv_len, 1)):
-        if t.dtype != torch.int32 or t.dim() != dims or t.device != cache.device:
-            raise ValueError("%s must be an int32 tensor of %d dimension(s) on %s" % (what, dims, cache.device))
-    seqs, width = table.shape
-    if q_start.shape[0] != seqs + 1 or kv_len.shape[0] != seqs:
-        raise ValueError("%d table rows need %d q_start and %d kv_len entries, got %d and %d"
-                         % (seqs, seqs + 1, seqs, q_start.shape[0], kv_len.shape[0]))
-    if (width > 1 and table.stride(1) != 1) or not q_start.is_contiguous() or not kv_len.is_contiguous():
-        raise ValueError("q_start, kv_len and the rows of table must be contiguous")
-    _need(width >= 1, "table has no columns")
-    return _Batch(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
-                  max(table.stride(0), width), width, seqs, tokens)
-
-
-def _heads(what, t, cache, heads, dim, tokens=None):
-    """A token-major tensor tokens x heads x dim of the cache's type and device."""
-    if t.dtype != cache.dtype or t.device != cache.device:
-        raise ValueError("%s has dtype %s on %s, the cache %s on %s" % (what, t.dtype, t.device, cache.dtype, cache.device))
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads) or (tokens is not None and shape[0] != tokens):
-        raise ValueError("%s has shape %s, expected %s x %s x %d" % (what, tuple(shape), tokens or "tokens", heads or "heads", dim))
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError("%s: the elements of a head must be contiguous" % what)
-    return s
-
-
 def kv_append(k, v, cache, table, q_start, kv_len, stream=None):
     """Write the new tokens' keys and values (tokens x kv_heads x head_dim) into their pages.
 
     table (seqs x pages), q_start (seqs + 1) and kv_len (seqs, the new tokens included) are int32 on
     the device; a token at a negative position or on an unmapped page is not written."""
-    ks = _heads("k", k, cache, cache.kv_heads, cache.head_dim)
-    vs = _heads("v", v, cache, cache.kv_heads, cache.head_dim, k.shape[0])
-    _need(ks == vs, "k and v have different strides %s and %s" % (ks, vs))
-    batch = _batch(cache, table, q_start, kv_len, k.shape[0])
-    _fail(_lib().blk_kv_append(cache._ref, batch, k.data_ptr(), v.data_ptr(), ks[0], ks[1],
-                               _raw_stream(stream, cache.device)), "kv_append")
+    rc = _ext().kv_append(cache._addr, k, v, table, q_start, kv_len, _raw_stream(stream, cache._index))
+    if rc:
+        _fail(rc, "kv_append")
 
 
 def kv_copy_pages(cache, src, dst, stream=None):
-    """Copy page src[i] to page dst[i], keys and values (lists of page numbers; no page twice in dst,
-    none in both)."""
-    n = len(src)
-    _need(len(dst) == n, "%d source pages, %d destinations" % (n, len(dst)))
-    pages = ctypes.c_int32 * n
-    _fail(_lib().blk_kv_copy_pages(cache._ref, pages(*src), pages(*dst), n, _raw_stream(stream, cache.device)),
-          "kv_copy_pages")
+    """Copy page src[i] to page dst[i], keys and values (sequences of page numbers; no page twice in
+    dst, none in both)."""
+    rc = _ext().kv_copy_pages(cache._addr, src, dst, _raw_stream(stream, cache._index))
+    if rc:
+        _fail(rc, "kv_copy_pages")
 
 
 class AttnWorkspace:
@@ -184,7 +149,7 @@ class AttnWorkspace:
         self.buffer = torch.zeros(self.bytes, dtype=torch.uint8, device=device)
         # Any stream may use it from here on.
         torch.cuda.current_stream(self.buffer.device).synchronize()
-        self._ptr = self.buffer.data_ptr()
+        self._ptr, self.index = self.buffer.data_ptr(), self.buffer.device.index
 
 
 def attn_run(q, cache, table, q_start, kv_len, out, ws, *, max_q=None, scale=None, window=0, gate=None, lse=None,
@@ -196,21 +161,12 @@ def attn_run(q, cache, table, q_start, kv_len, out, ws, *, max_q=None, scale=Non
     key heads in groups. lse (float32, tokens x heads) receives the log of the sums of exponentials.
     max_q is the largest number of new tokens of a sequence (default: all of them): it picks the
     kernel, not the result."""
-    tokens, heads, dim = q.shape
-    _need(dim == cache.head_dim and heads % cache.kv_heads == 0,
-          "q has %d heads of %d, the cache %d of %d" % (heads, dim, cache.kv_heads, cache.head_dim))
-    qs = _heads("q", q, cache, heads, dim)
-    os = _heads("out", out, cache, heads, dim, tokens)
-    gs = _heads("gate", gate, cache, heads, dim, tokens) if gate is not None else (0, 0)
-    if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.shape == (tokens, heads) and lse.is_contiguous() and lse.device == cache.device,
-              "lse must be a contiguous float32 tensor %d x %d on %s" % (tokens, heads, cache.device))
-    _need(ws.buffer.device == cache.device and ws.head_dim >= dim, "the workspace is for head_dim %d on %s" % (ws.head_dim, ws.buffer.device))
-    args = _Attn(q.data_ptr(), gate.data_ptr() if gate is not None else None, out.data_ptr(),
-                 lse.data_ptr() if lse is not None else None, qs[0], qs[1], gs[0], gs[1], os[0], os[1], heads,
-                 max(tokens, 1) if max_q is None else max_q, window, dim ** -0.5 if scale is None else scale)
-    batch = _batch(cache, table, q_start, kv_len, tokens)
-    _fail(_lib().blk_attn_run(cache._ref, batch, args, ws._ptr, ws.bytes, _raw_stream(stream, cache.device)), "attn_run")
+    if ws.head_dim < cache.head_dim or ws.index != cache._index:
+        raise ValueError("the workspace is for head_dim %d on GPU %d" % (ws.head_dim, ws.index))
+    rc = _ext().attn_run(cache._addr, ws._ptr, ws.bytes, q, table, q_start, kv_len, out, gate, lse, max_q, scale, window,
+                         _raw_stream(stream, cache._index))
+    if rc:
+        _fail(rc, "attn_run")
 
 
 # ------------------------------------------------------------- 4-bit projections
@@ -221,7 +177,7 @@ class W4Weight:
     def __init__(self, shape, packed, dtype):
         self.n, self.k, self.group = shape.n, shape.k, shape.group
         self.packed, self.dtype, self.device = packed, dtype, packed.device
-        self._ref, self._ptr = ctypes.byref(shape), packed.data_ptr()
+        self._addr, self._ptr, self._index = ctypes.addressof(shape), packed.data_ptr(), packed.device.index
         self._shape = shape
 
 
@@ -249,17 +205,9 @@ def w4_prepare(q, scales, zeros=None, group=128):
 
 def w4_run(w, x, out, stream=None):
     """out (m x n) = x (m x k) @ W^T with 4-bit weights; rows of x and out may be strided."""
-    if x.dtype != w.dtype or out.dtype != w.dtype or x.device != w.device or out.device != w.device:
-        raise ValueError("x is %s on %s, out %s on %s, the weights %s on %s"
-                         % (x.dtype, x.device, out.dtype, out.device, w.dtype, w.device))
-    m = x.shape[0]
-    if x.dim() != 2 or out.dim() != 2 or x.shape[1] != w.k or out.shape[0] != m or out.shape[1] != w.n:
-        raise ValueError("x has shape %s, out %s, expected m x %d and m x %d" % (tuple(x.shape), tuple(out.shape), w.k, w.n))
-    xs, os = x.stride(), out.stride()
-    if xs[1] != 1 or (os[1] != 1 and w.n > 1):
-        raise ValueError("the rows of x and out must be contiguous")
-    _fail(_lib().blk_w4_run(w._ref, w._ptr, x.data_ptr(), xs[0], m, out.data_ptr(), os[0],
-                            _raw_stream(stream, w.device)), "w4_run")
+    rc = _ext().w4_run(w._addr, w._ptr, x, out, _raw_stream(stream, w._index))
+    if rc:
+        _fail(rc, "w4_run")
 
 
 # ------------------------------------------------------------- norms around a block
@@ -271,39 +219,7 @@ def norm_run(x, residual, out, *, weight_pre, weight_post=None, gate=None, alpha
     x: a block's output (m x width), or None for the norm before the first block; residual: m x width
     of x's type or float32; gate: width, or m x width; without weight_post x is added as it is.
     residual_out defaults to residual, updated in place."""
-    _need(out.dim() == 2 and out.dtype in (torch.bfloat16, torch.float16) and out.is_cuda,
-          "out must be a bfloat16 or float16 device tensor m x width")
-    m, width = out.shape
-    dtype, device = out.dtype, out.device
-    _need(residual.dtype in (dtype, torch.float32), "residual has dtype %s, expected %s or float32" % (residual.dtype, dtype))
-    if x is None:
-        _need(weight_post is None and gate is None and residual_out is None, "weight_post, gate and residual_out need x")
-    elif residual_out is None:
-        residual_out = residual
-
-    def rows(what, t, kind):
-        if t is None:
-            return None, 0
-        if t.dtype != kind or t.device != device or t.shape != (m, width) or (t.stride(1) != 1 and width > 1):
-            raise ValueError("%s must be %s on %s, %d x %d, with contiguous rows" % (what, kind, device, m, width))
-        return t.data_ptr(), t.stride(0)
-
-    def vector(what, t):
-        if t is None:
-            return None
-        if t.dtype != dtype or t.device != device or t.shape != (width,) or (t.stride(0) != 1 and width > 1):
-            raise ValueError("%s must be a contiguous %s vector of %d on %s" % (what, dtype, width, device))
-        return t.data_ptr()
-
-    _need(weight_pre is not None, "weight_pre is needed")
-    xp, xs = rows("x", x, dtype)
-    rp, rs = rows("residual", residual, residual.dtype)
-    yp, ys = rows("residual_out", residual_out, residual.dtype)
-    op, os = rows("out", out, dtype)
-    if gate is not None and gate.dim() == 1:
-        gp, gs = vector("gate", gate), 0
-    else:
-        gp, gs = rows("gate", gate, dtype)
-    args = _Norm(xp, rp, gp, vector("weight_post", weight_post), vector("weight_pre", weight_pre), yp, op,
-                 xs, rs, gs, ys, os, width, DTYPES[dtype], DTYPES[residual.dtype], alpha, eps)
-    _fail(_lib().blk_norm_run(args, m, _raw_stream(stream, device)), "norm_run")
+    rc = _ext().norm_run(x, residual, out, weight_pre, weight_post, gate, alpha, eps, residual_out,
+                         _raw_stream(stream, out.device.index) if out.is_cuda else 0)
+    if rc:
+        _fail(rc, "norm_run")

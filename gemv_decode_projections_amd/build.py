@@ -15,6 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(LIBDIR, "libgdproj.so")
+EXT = os.path.join(LIBDIR, "_block.so")
 
 SOURCES = [
     "proj_api.hip",
@@ -74,6 +75,28 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_ext(verbose):
+    """The compiled Python entries of the block operators (csrc/block_py.cpp), host code against torch."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    tmp = EXT + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I" + os.path.join(root, "include"), "-I" + os.path.join(root, "include/torch/csrc/api/include"),
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "block_py.cpp"), "-o", tmp,
+           "-L" + LIBDIR, "-lgdproj", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(root, "lib"),
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for block_py.cpp:\n%s" % r.stderr)
+    os.replace(tmp, EXT)
+
+
 def build(verbose=False, jobs=None):
     os.makedirs(LIBDIR, exist_ok=True)
     os.makedirs(OBJDIR, exist_ok=True)
@@ -86,6 +109,7 @@ def build(verbose=False, jobs=None):
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _build_ext(verbose)
     return LIB
 
 

@@ -294,6 +294,8 @@ __device__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
     u.row0 = tile * ROWS;
     u.nrows = min(ROWS, u.n * a.group - u.row0);
     u.lo += u.split * part.c;
+    if (a.window > 0)
+        u.lo = max(u.lo, (u.len - u.n + a.by_group(u.row0) - a.window + 1) & -a.kv_step);
     // The tile's last token sees no further than its own position.
     const int last = u.len - u.n + a.by_group(u.row0 + u.nrows - 1);
     u.hi = min(u.split + 1 < u.splits ? u.lo + part.c : u.len, max(last + 1, 0));
