@@ -14,15 +14,25 @@ namespace {
 
 // One 16-byte piece of a new token's key or value per thread: a pure copy,
 // bound by the launch at decode sizes and by HBM at a prompt's.
-__global__ __launch_bounds__(256) void kv_append_kernel(AttnArgs a, const char *kin, const char *vin, int64_t in_stride,
-                                                        int64_t in_head, int per_head, int per_token, int64_t total)
+struct AppendArgs {
+    AttnArgs a;
+    const char *k, *v;
+    int64_t in_stride, in_head;        // bytes
+    int64_t total;                     // 16-byte pieces of k
+    int per_head;                      // of them in a head
+    Divisor by_token, by_head;         // of the pieces of a token, of a head
+};
+
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs x)
 {
+    const AttnArgs &a = x.a;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= total)
+    if (id >= x.total)
         return;
-    const int tok = (int)(id / per_token);
-    const int piece = (int)(id - (int64_t)tok * per_token);
-    const int head = piece / per_head;
+    const int per_head = x.per_head, per_token = per_head * a.kv_heads;
+    const int tok = x.by_token((int)id);
+    const int piece = (int)id - tok * per_token;
+    const int head = x.by_head(piece);
     const int at = (piece - head * per_head) * 16;
     // The token's sequence: the last whose first row is not past it.
     int lo = 0, hi = a.seqs;
@@ -43,9 +53,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AttnArgs a, const char *
     int64_t off;
     if (!kv_offset(a, a.table[lo * a.table_stride + (pos >> a.page_shift)], pos, (int64_t)head * a.head_stride, off))
         return;
-    const int64_t from = tok * in_stride + head * in_head + at;
-    const u32x4 k = *reinterpret_cast<const u32x4 *>(kin + from);
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(vin + from);
+    const int64_t from = tok * x.in_stride + head * x.in_head + at;
+    const u32x4 k = *reinterpret_cast<const u32x4 *>(x.k + from);
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(x.v + from);
     *reinterpret_cast<u32x4 *>(const_cast<char *>(a.k) + off + at) = k;
     *reinterpret_cast<u32x4 *>(const_cast<char *>(a.v) + off + at) = v;
 }
@@ -171,17 +181,21 @@ int blk_kv_append(const blk_cache *cache, const blk_batch *batch, const void *k,
         return PROJ_ERR_NULL;
     if (!aligned_to(k, 16) || !aligned_to(v, 16))
         return PROJ_ERR_ALIGN;
-    AttnArgs a = base_args(cache, batch);
-    int per_head = cache->head_dim / 8, per_token = per_head * cache->kv_heads;
-    int64_t total = (int64_t)batch->tokens * per_token;
-    if ((total + 255) / 256 > 0x7fffffff)
+    AppendArgs x{};
+    x.a = base_args(cache, batch);
+    x.per_head = cache->head_dim / 8;
+    const int64_t per_token = (int64_t)x.per_head * cache->kv_heads;
+    x.total = batch->tokens * per_token;
+    if (x.total > 0x7fffffff)
         return PROJ_ERR_ARG;
-    const char *kin = static_cast<const char *>(k), *vin = static_cast<const char *>(v);
-    int64_t stride = in_stride * 2, head = in_head_stride * 2;
-    hipLaunchKernelGGL(kv_append_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), a, kin, vin, stride, head, per_head, per_token, total);
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? PROJ_OK : hip_fail(e);
+    x.by_token = Divisor::of((uint32_t)per_token);
+    x.by_head = Divisor::of((uint32_t)x.per_head);
+    x.k = static_cast<const char *>(k);
+    x.v = static_cast<const char *>(v);
+    x.in_stride = in_stride * 2;
+    x.in_head = in_head_stride * 2;
+    return launch(reinterpret_cast<const void *>(kv_append_kernel), dim3((unsigned)((x.total + 255) / 256)), dim3(256), &x,
+                  stream);
 }
 
 int blk_kv_copy_pages(const blk_cache *cache, const int32_t *src, const int32_t *dst, int n, void *stream)

@@ -14,7 +14,7 @@
 //
 // Memory bound at the token counts it is for (16 tokens: 64 operations per
 // weight byte). A workgroup owns RB blocks of 16 rows and 16 NT tokens; its
-// eight waves split K, each unit of 128 k is one 16-byte load per lane and row
+// waves split K, each unit of 128 k is one 16-byte load per lane and row
 // block, 1 KB contiguous per wave.
 #include <limits.h>
 
@@ -24,7 +24,6 @@ namespace gdp {
 namespace {
 
 constexpr int kUnitK = 128;            // k per 16-byte load of a lane
-constexpr int kW4Waves = 8;
 
 struct W4Args {
     const u32x4 *w;                    // [row block][unit][lane]
@@ -45,24 +44,45 @@ __device__ __forceinline__ uint32_t weight_pair(uint32_t w, int j)
     return ((w >> (4 * j)) & 0x000f000fu) | magic;
 }
 
-template <class T, int G, int RB, int NT>
-__global__ __launch_bounds__(64 * kW4Waves) void w4_kernel(W4Args a)
+// CH units of a wave are loaded at once, weights, scales and activations, all
+// in flight before the first product.
+//
+// Activations are read along the rows, 256 bytes per 16 lanes, and turned to
+// operands (column l % 16, k 8 (l / 16) + 0..7 of each 32) by way of LDS,
+// 16-byte pieces permuted so that neither side meets a bank conflict: read as
+// operands, every four lanes would touch four rows (2304 x 8192, 16 tokens:
+// 10.2 us, this way 6.5). DIRECT reads them as operands all the same: for one
+// or two tokens the lanes' rows coincide (one token: 5.5 us against 6.1).
+template <class T, int G, int RB, int NT, int CH, int WAVES, bool DIRECT>
+__global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a)
 {
     constexpr bool BF = T::kId == BLK_BF16;
     constexpr int GPU_ = kUnitK / G;   // groups per unit
     constexpr int SPG = G / 32;        // k-steps per group
-    __shared__ f32x4 s_part[kW4Waves][RB * NT][kWave];
+    // Each wave's activations of a unit, 16 tokens x 256 bytes per block; at the
+    // end the waves' sums.
+    constexpr int XB = 16 * kUnitK * 2;
+    constexpr int LDSB = WAVES * (NT * XB > RB * NT * 1024 ? NT * XB : RB * NT * 1024);
+    __shared__ __align__(16) char s_mem[LDSB];
+    f32x4(&s_part)[WAVES][RB * NT][kWave] = *reinterpret_cast<f32x4(*)[WAVES][RB * NT][kWave]>(s_mem);
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int col = lane % 16, quad = lane / 16;
     const int rb0 = blockIdx.x * RB;
     const int tok0 = blockIdx.y * 16 * NT;
-    const int u0 = (int)((int64_t)wave * a.units / kW4Waves), u1 = (int)((int64_t)(wave + 1) * a.units / kW4Waves);
+    const int u0 = (int)((int64_t)wave * a.units / WAVES), u1 = (int)((int64_t)(wave + 1) * a.units / WAVES);
 
-    const char *xp[NT];
+    char *xl = s_mem + wave * NT * XB;
+    const char *xp[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-        xp[t] = a.x + (int64_t)min(tok0 + 16 * t + col, a.m - 1) * a.x_stride + quad * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            xp[t][i] = a.x + (int64_t)min(tok0 + 16 * t + (DIRECT ? col : 4 * i + quad), a.m - 1) * a.x_stride;
+    int64_t block[RB];                 // the row blocks' first units; past the last block, the last again
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+        block[r] = (int64_t)min(rb0 + r, a.blocks - 1) * a.units;
 
     f32x4 acc[RB][NT];
 #pragma unroll
@@ -70,89 +90,122 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_kernel(W4Args a)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint32_t one = BF ? 0x3f803f80u : 0x3c003c00u;
+    const uint32_t one = 0x3f803f80u;
     const u32x4 ones = {one, one, one, one};
 
-    for (int u = u0; u < u1; ++u) {
-        u32x4 w[RB];
+    for (int first = u0; first < u1; first += CH) {
+        u32x4 w[CH][RB], xf[CH][NT][4];
+        u32x2 sc[CH][GPU_][RB], zc[CH][GPU_][RB];
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-            w[r] = a.w[((int64_t)min(rb0 + r, a.blocks - 1) * a.units + u) * kWave + lane];
-        u32x4 xf[NT][4];
+        for (int c = 0; c < CH; ++c) {
+            // Units past the wave's last load that one again; k past the
+            // matrix loads its last eight again. Neither is used.
+            const int u = min(first + c, u1 - 1);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-            if (u * kUnitK + 32 * s < a.k)
+            for (int r = 0; r < RB; ++r)
+                w[c][r] = a.w[(block[r] + u) * kWave + lane];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    xf[t][s] = *reinterpret_cast<const u32x4 *>(xp[t] + ((int64_t)u * kUnitK + 32 * s) * 2);
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int g = 0; g < GPU_; ++g) {
-            if (u * kUnitK + G * g >= a.k)
-                break;
-            f32x4 xs[NT];
-            if constexpr (BF)
+                for (int i = 0; i < 4; ++i)
+                    xf[c][t][i] = *reinterpret_cast<const u32x4 *>(
+                        xp[t][i] + (int64_t)min(u * kUnitK + 8 * (DIRECT ? 4 * i + quad : col), a.k - 8) * 2);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    xs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int g = 0; g < GPU_; ++g)
 #pragma unroll
-                    for (int s = 0; s < SPG; ++s)
-                        xs[t] = T::mfma16(ones, xf[t][g * SPG + s], xs[t]);
-                }
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                const int64_t group = (((int64_t)min(rb0 + r, a.blocks - 1) * a.units + u) * GPU_ + g) * 32;
-                const u32x2 sc = *reinterpret_cast<const u32x2 *>(a.scale + group + quad * 8);
-                u32x2 zc = {BF ? 0x43084308u : 0u, BF ? 0x43084308u : 0u};
-                uint32_t zrow = 0x64086408u;
-                if (a.zero) {
-                    if constexpr (BF)
-                        zc = *reinterpret_cast<const u32x2 *>(a.zero + group + quad * 8);
-                    else
-                        zrow = *reinterpret_cast<const uint16_t *>(a.zero + group + col * 2) * 0x10001u;
-                }
-                f32x4 part[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    part[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < SPG; ++s) {
-                    u32x4 wf;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t p = weight_pair<T>(w[r][g * SPG + s], j);
-                        if constexpr (!BF)
-                            p = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) - __builtin_bit_cast(f16x2, zrow));
-                        wf[j] = p;
+                for (int r = 0; r < RB; ++r) {
+                    const int64_t group = ((block[r] + u) * GPU_ + g) * 32;
+                    sc[c][g][r] = *reinterpret_cast<const u32x2 *>(a.scale + group + quad * 8);
+                    zc[c][g][r] = u32x2{BF ? 0x43084308u : 0x64086408u, 0x43084308u};
+                    if (a.zero) {
+                        if constexpr (BF)
+                            zc[c][g][r] = *reinterpret_cast<const u32x2 *>(a.zero + group + quad * 8);
+                        else
+                            zc[c][g][r].x = *reinterpret_cast<const uint16_t *>(a.zero + group + col * 2) * 0x10001u;
                     }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        part[t] = T::mfma16(wf, xf[t][g * SPG + s], part[t]);
                 }
-                const float sf[4] = {T::lo(sc.x), T::hi(sc.x), T::lo(sc.y), T::hi(sc.y)};
-                const float zf[4] = {T::lo(zc.x), T::hi(zc.x), T::lo(zc.y), T::hi(zc.y)};
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if (first + c >= u1)
+                break;
+            if constexpr (!DIRECT) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float v = part[t][i];
-                        if constexpr (BF)
-                            v -= zf[i] * xs[t][i];
-                        acc[r][t][i] += sf[i] * v;
+                        const int tok = 4 * i + quad;
+                        *reinterpret_cast<u32x4 *>(xl + t * XB + tok * 256 + (col ^ tok) * 16) = xf[c][t][i];
                     }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        xf[c][t][s] =
+                            *reinterpret_cast<const u32x4 *>(xl + t * XB + col * 256 + ((4 * s + quad) ^ col) * 16);
+            }
+#pragma unroll
+            for (int g = 0; g < GPU_; ++g) {
+                if ((first + c) * kUnitK + G * g >= a.k)
+                    break;
+                f32x4 xs[NT];
+                if constexpr (BF)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        xs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int s = 0; s < SPG; ++s)
+                            xs[t] = T::mfma16(ones, xf[c][t][g * SPG + s], xs[t]);
+                    }
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    f32x4 part[NT];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        part[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    const uint32_t zrow = zc[c][g][r].x;
+#pragma unroll
+                    for (int s = 0; s < SPG; ++s) {
+                        u32x4 wf;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t p = weight_pair<T>(w[c][r][g * SPG + s], j);
+                            if constexpr (!BF)
+                                p = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) - __builtin_bit_cast(f16x2, zrow));
+                            wf[j] = p;
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            part[t] = T::mfma16(wf, xf[c][t][g * SPG + s], part[t]);
+                    }
+                    const u32x2 s2 = sc[c][g][r], z2 = zc[c][g][r];
+                    const float sf[4] = {T::lo(s2.x), T::hi(s2.x), T::lo(s2.y), T::hi(s2.y)};
+                    const float zf[4] = {T::lo(z2.x), T::hi(z2.x), T::lo(z2.y), T::hi(z2.y)};
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float v = part[t][i];
+                            if constexpr (BF)
+                                v -= zf[i] * xs[t][i];
+                            acc[r][t][i] += sf[i] * v;
+                        }
+                }
             }
         }
     }
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             s_part[wave][r * NT + t][lane] = acc[r][t];
     __syncthreads();
-    for (int i = wave; i < RB * NT; i += kW4Waves) {
+    for (int i = wave; i < RB * NT; i += WAVES) {
         const int r = i / NT, t = i % NT;
         f32x4 v = s_part[0][i][lane];
 #pragma unroll
-        for (int w = 1; w < kW4Waves; ++w)
+        for (int w = 1; w < WAVES; ++w)
             v += s_part[w][i][lane];
         const int tok = tok0 + 16 * t + col;
         const int row = (rb0 + r) * 16 + 4 * quad;
@@ -218,18 +271,42 @@ __global__ void w4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
     }
 }
 
-using W4Kernel = void (*)(W4Args);
+struct W4Plan {
+    void (*fn)(W4Args);
+    int rb, nt, waves;
+};
 
+// Tiles by token count and row blocks; measured (us) on the shapes in brackets.
 template <class T, int G>
-W4Kernel pick(int nt)
+W4Plan pick(int m, int blocks, int units)
 {
-    return nt == 1 ? w4_kernel<T, G, 1, 1> : nt == 2 ? w4_kernel<T, G, 2, 2> : w4_kernel<T, G, 2, 4>;
+    const bool many = blocks >= 512;       // two row blocks per workgroup still fill the chip
+    if (m <= 16) {
+        // Short k: one unit per wave and turn.
+        if (units < 32)
+            return many ? W4Plan{w4_kernel<T, G, 2, 1, 1, 8, false>, 2, 1, 8}
+                        : W4Plan{w4_kernel<T, G, 1, 1, 1, 8, false>, 1, 1, 8};
+        if (m <= 2)
+            return {w4_kernel<T, G, 1, 1, 4, 8, true>, 1, 1, 8};
+        return {w4_kernel<T, G, 1, 1, 2, 16, false>, 1, 1, 16};
+    }
+    // 8192 x 4096, 32 tokens: 9.6 with two row blocks and 16 waves, 12.6 with
+    // one; 2304 x 8192: 11.7 and 10.3.
+    if (m <= 32 && !many)
+        return {w4_kernel<T, G, 1, 2, 2, 8, false>, 1, 2, 8};
+    // 64 tokens in two tiles, 8192 x 4096: 15.2 with four row blocks, 17.6 with
+    // two; 2304 x 8192: 18.1 and 12.3.
+    if (m > 32 && many)
+        return {w4_kernel<T, G, 4, 2, 2, 8, false>, 4, 2, 8};
+    return {w4_kernel<T, G, 2, 2, 1, 16, false>, 2, 2, 16};
 }
 
 template <class T>
-W4Kernel pick(int group, int nt)
+W4Plan pick(int group, int m, int blocks, int units)
 {
-    return group == 32 ? pick<T, 32>(nt) : group == 64 ? pick<T, 64>(nt) : pick<T, 128>(nt);
+    return group == 32   ? pick<T, 32>(m, blocks, units)
+           : group == 64 ? pick<T, 64>(m, blocks, units)
+                         : pick<T, 128>(m, blocks, units);
 }
 
 struct Layout {
@@ -324,13 +401,13 @@ int blk_w4_run(const blk_w4 *w, const void *packed, const void *x, int64_t x_str
     a.units = l.units;
     a.blocks = l.blocks;
     a.wide_out = w->n % 4 == 0 && out_stride % 4 == 0 && aligned_to(out, 8);
-    const int nt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
-    const int rb = nt == 1 ? 1 : 2;
-    W4Kernel fn = w->dtype == BLK_BF16 ? pick<BF16>(w->group, nt) : pick<F16>(w->group, nt);
+    const W4Plan plan = w->dtype == BLK_BF16 ? pick<BF16>(w->group, m, l.blocks, l.units)
+                                             : pick<F16>(w->group, m, l.blocks, l.units);
     void *params[1] = {&a};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(fn),
-                                         dim3((l.blocks + rb - 1) / rb, (m + 16 * nt - 1) / (16 * nt)),
-                                         dim3(64 * kW4Waves), params, 0, static_cast<hipStream_t>(stream));
+    const hipError_t e = hipLaunchKernel(
+        reinterpret_cast<const void *>(plan.fn),
+        dim3((l.blocks + plan.rb - 1) / plan.rb, (m + 16 * plan.nt - 1) / (16 * plan.nt)), dim3(64 * plan.waves), params,
+        0, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? PROJ_OK : hip_fail(e);
 }
 
