@@ -23,6 +23,7 @@ import torch
 from . import binding as _b
 
 _i, _i64, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
+_pages = ctypes.POINTER(ctypes.c_int32)
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 HEAD_DIMS = (64, 128, 256)
@@ -50,6 +51,14 @@ def _lib():
         shape = ctypes.POINTER(_W4)
         sig = {
             "blk_attn_workspace_bytes": ([_i], ctypes.c_size_t),
+            "blk_pool_create": ([_i, ctypes.POINTER(_vp)], _i),
+            "blk_pool_destroy": ([_vp], None),
+            "blk_pool_free_pages": ([_vp], _i),
+            "blk_pool_users": ([_vp, ctypes.c_int32], _i),
+            "blk_pool_alloc": ([_vp, _i, _pages], _i),
+            "blk_pool_share": ([_vp, _pages, _i], _i),
+            "blk_pool_release": ([_vp, _pages, _i], _i),
+            "blk_pool_compact": ([_vp, _i, _pages, _pages], _i),
             "blk_w4_packed_bytes": ([shape], ctypes.c_size_t),
             "blk_w4_pack": ([shape, _vp, _vp, _vp, _vp, _vp], _i),
         }
@@ -136,6 +145,76 @@ def kv_copy_pages(cache, src, dst, stream=None):
     rc = _ext().kv_copy_pages(cache._addr, src, dst, _raw_stream(stream, cache._index))
     if rc:
         _fail(rc, "kv_copy_pages")
+
+
+class PagePool:
+    """Which pages of a cache are in use, and by how many sequences (host memory only).
+
+    A sequence is the caller's list of pages. fork shares them; a page to be written that other
+    sequences use too is first replaced by writable(), which says what to copy."""
+
+    def __init__(self, n_pages):
+        self.n_pages = int(n_pages)
+        handle = _vp()
+        _fail(_lib().blk_pool_create(self.n_pages, ctypes.byref(handle)), "PagePool(%d)" % self.n_pages)
+        self._handle = handle
+
+    def __del__(self):
+        handle, self._handle = getattr(self, "_handle", None), None
+        if handle and _LIB is not None:
+            _LIB.blk_pool_destroy(handle)
+
+    @property
+    def free_pages(self):
+        return _lib().blk_pool_free_pages(self._handle)
+
+    def users(self, page):
+        n = _lib().blk_pool_users(self._handle, page)
+        _fail(min(n, 0), "users(%d)" % page)
+        return n
+
+    def alloc(self, n):
+        """The n lowest free pages; ProjError (PROJ_ERR_PAGES), and none taken, if there are fewer."""
+        pages = (ctypes.c_int32 * max(n, 0))()
+        _fail(_lib().blk_pool_alloc(self._handle, n, pages), "alloc(%d)" % n)
+        return list(pages)
+
+    def fork(self, pages):
+        """Another sequence's list of the same pages: each gets one more user."""
+        _fail(_lib().blk_pool_share(self._handle, (ctypes.c_int32 * len(pages))(*pages), len(pages)), "fork")
+        return list(pages)
+
+    def free(self, pages):
+        """Takes one user from each page; pages without users are free again."""
+        _fail(_lib().blk_pool_release(self._handle, (ctypes.c_int32 * len(pages))(*pages), len(pages)), "free")
+
+    def writable(self, pages, index):
+        """Makes pages[index] this sequence's own before a write: (old, new) to be copied if others
+        use it too (the list then names new), None if they do not."""
+        old = pages[index]
+        users = self.users(old)
+        _need(users > 0, "page %d is not in use" % old)
+        if users == 1:
+            return None
+        new = self.alloc(1)[0]
+        self.free([old])
+        pages[index] = new
+        return old, new
+
+    def compact(self, max_moves=None):
+        """Moves of pages down into free ones: (src, dst), as kv_copy_pages takes them. Replace src[i]
+        by dst[i] in every page list (remap) and table."""
+        n = self.n_pages if max_moves is None else max_moves
+        src, dst = (ctypes.c_int32 * max(n, 0))(), (ctypes.c_int32 * max(n, 0))()
+        moves = _lib().blk_pool_compact(self._handle, n, src, dst)
+        _fail(min(moves, 0), "compact(%s)" % max_moves)
+        return src[:moves], dst[:moves]
+
+    @staticmethod
+    def remap(pages, src, dst):
+        """The page list after the moves."""
+        to = dict(zip(src, dst))
+        return [to.get(p, p) for p in pages]
 
 
 class AttnWorkspace:

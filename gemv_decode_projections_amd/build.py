@@ -35,6 +35,7 @@ SOURCES = [
     "attn_join.hip",
     "w4.hip",
     "norm.hip",
+    "page_pool.cpp",
 ]
 
 ARCH = os.environ.get("GDP_OFFLOAD_ARCH", "gfx950")

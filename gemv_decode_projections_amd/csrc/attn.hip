@@ -61,19 +61,23 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs x)
 }
 
 // Page pairs travel in the kernel's arguments: no device list to allocate,
-// copy or keep alive, and a graph keeps its own.
-constexpr int kPairs = 448;
+// copy or keep alive, and a graph keeps its own. Page numbers of 16 bits fit
+// twice as many in the 4 KB that a launch takes (1500 moves of 64 KB pages: two
+// launches instead of four).
+template <class I>
 struct CopyArgs {
+    static constexpr int kPairs = 1792 / sizeof(I);
     char *k, *v;
     int64_t page_stride;       // bytes
     int page_bytes;
-    int32_t src[kPairs], dst[kPairs];
+    I src[kPairs], dst[kPairs];
 };
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;         // 16-byte pieces per thread, all loads in flight
 
-__global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(CopyArgs a)
+template <class I>
+__global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(CopyArgs<I> a)
 {
     char *base = blockIdx.z ? a.v : a.k;
     const char *src = base + a.src[blockIdx.y] * a.page_stride;
@@ -158,6 +162,28 @@ int launch(const void *fn, dim3 grid, dim3 block, void *arg, void *stream)
     return e == hipSuccess ? PROJ_OK : hip_fail(e);
 }
 
+template <class I>
+int copy_pages(const blk_cache *cache, const int32_t *src, const int32_t *dst, int n, int64_t elems, void *stream)
+{
+    typedef CopyArgs<I> Args;
+    Args a{};
+    a.k = static_cast<char *>(cache->k);
+    a.v = static_cast<char *>(cache->v);
+    a.page_stride = cache->page_stride * 2;
+    a.page_bytes = (int)(elems * 2);
+    const int per_wg = kCopyThreads * kCopyUnroll * 16;
+    for (int i = 0; i < n; i += Args::kPairs) {
+        const int c = std::min(Args::kPairs, n - i);
+        std::copy(src + i, src + i + c, a.src);
+        std::copy(dst + i, dst + i + c, a.dst);
+        const int rc = launch(reinterpret_cast<const void *>(kv_copy_kernel<I>),
+                              dim3((unsigned)((a.page_bytes + per_wg - 1) / per_wg), c, 2), dim3(kCopyThreads), &a, stream);
+        if (rc)
+            return rc;
+    }
+    return PROJ_OK;
+}
+
 }  // namespace
 }  // namespace gdp
 
@@ -233,22 +259,8 @@ int blk_kv_copy_pages(const blk_cache *cache, const int32_t *src, const int32_t 
     } catch (const std::bad_alloc &) {
         return PROJ_ERR_HIP;
     }
-    CopyArgs a{};
-    a.k = static_cast<char *>(cache->k);
-    a.v = static_cast<char *>(cache->v);
-    a.page_stride = cache->page_stride * 2;
-    a.page_bytes = (int)(elems * 2);
-    const unsigned per_page = (unsigned)((a.page_bytes + kCopyThreads * kCopyUnroll * 16 - 1) / (kCopyThreads * kCopyUnroll * 16));
-    for (int i = 0; i < n; i += kPairs) {
-        const int c = std::min(kPairs, n - i);
-        memcpy(a.src, src + i, c * sizeof(int32_t));
-        memcpy(a.dst, dst + i, c * sizeof(int32_t));
-        const int rc2 = launch(reinterpret_cast<const void *>(kv_copy_kernel), dim3(per_page, c, 2),
-                               dim3(kCopyThreads), &a, stream);
-        if (rc2)
-            return rc2;
-    }
-    return PROJ_OK;
+    return cache->n_pages <= 65536 ? copy_pages<uint16_t>(cache, src, dst, n, elems, stream)
+                                   : copy_pages<int32_t>(cache, src, dst, n, elems, stream);
 }
 
 size_t blk_attn_workspace_bytes(int head_dim) { return head_dim > 0 && head_dim <= 256 ? attn_ws_bytes(head_dim) : 0; }

@@ -92,6 +92,33 @@ int blk_kv_append(const blk_cache *cache, const blk_batch *batch, const void *k,
 int blk_kv_copy_pages(const blk_cache *cache, const int32_t *src, const int32_t *dst, int n, void *stream);
 
 /*
+ * Page pool: which pages of a cache are in use, on the host. A page has a
+ * number of users: alloc gives it one, share (a fork: the sequences share the
+ * page) adds one, release takes one away, and without users it is free. alloc
+ * takes the lowest free pages. share and release do all or nothing:
+ * PROJ_ERR_ARG if a page is not in use (or released more often than used).
+ * PROJ_ERR_PAGES if fewer than n pages are free (none is taken then).
+ *
+ * blk_pool_compact moves pages from the top of the cache to free pages below:
+ * up to max_moves pairs into src and dst, returns their number (0: nothing to
+ * move, every page in use lies below every free one). The pool counts the
+ * pages as moved; the caller copies them (blk_kv_copy_pages takes the pairs as
+ * they are) and replaces src[i] by dst[i] in its page tables.
+ *
+ * Calls on one pool must not race each other.
+ */
+typedef struct blk_pool blk_pool;
+
+int blk_pool_create(int n_pages, blk_pool **pool);
+void blk_pool_destroy(blk_pool *pool);
+int blk_pool_free_pages(const blk_pool *pool);
+int blk_pool_users(const blk_pool *pool, int32_t page);
+int blk_pool_alloc(blk_pool *pool, int n, int32_t *pages);
+int blk_pool_share(blk_pool *pool, const int32_t *pages, int n);
+int blk_pool_release(blk_pool *pool, const int32_t *pages, int n);
+int blk_pool_compact(blk_pool *pool, int max_moves, int32_t *src, int32_t *dst);
+
+/*
  * blk_attn_run - attention of the new tokens over the cache:
  *     out[t, h] = sum_j softmax_j(scale * q[t, h] . K[j]) V[j]   [* sigmoid(gate[t, h])]
  * over the positions j that token t sees: j <= its own position, and with

@@ -13,14 +13,12 @@ TINY = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -25, torch.float32: 2
 def gather(cache, table_row, length):
     """The first `length` positions of one sequence (float64; NaN where the page is unmapped) and which are mapped."""
     pages, size, heads, dim = cache.shape
-    out = torch.full((length, heads, dim), math.nan, dtype=torch.float64)
-    held = torch.zeros(length, dtype=torch.bool)
-    c = cache.cpu()
-    for p in range(length):
-        page = int(table_row[p // size])
-        if 0 <= page < pages:
-            out[p] = c[page, p % size].double()
-            held[p] = True
+    at = torch.arange(length)
+    page = table_row.long()[at // size]
+    held = (page >= 0) & (page < pages)
+    device = cache.device
+    out = cache[page.clamp(0, pages - 1).to(device), (at % size).to(device)].cpu().double()
+    out[~held] = math.nan
     return out, held
 
 
