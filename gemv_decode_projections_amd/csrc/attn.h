@@ -293,12 +293,13 @@ __device__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
         return false;
     u.row0 = tile * ROWS;
     u.nrows = min(ROWS, u.n * a.group - u.row0);
-    u.lo += u.split * part.c;
-    if (a.window > 0)
-        u.lo = max(u.lo, (u.len - u.n + a.by_group(u.row0) - a.window + 1) & -a.kv_step);
-    // The tile's last token sees no further than its own position.
-    const int last = u.len - u.n + a.by_group(u.row0 + u.nrows - 1);
-    u.hi = min(u.split + 1 < u.splits ? u.lo + part.c : u.len, max(last + 1, 0));
+    // The part, less what no row of the tile sees: its last token sees no
+    // further than its own position, its first no further back than the window.
+    const int lo = u.lo + u.split * part.c;
+    const int hi = u.split + 1 < u.splits ? lo + part.c : u.len;
+    const int before = u.len - u.n;
+    u.lo = a.window > 0 ? max(lo, (before + a.by_group(u.row0) - a.window + 1) & -a.kv_step) : lo;
+    u.hi = min(hi, max(before + a.by_group(u.row0 + u.nrows - 1) + 1, 0));
     return true;
 }
 

@@ -214,7 +214,8 @@ def test_many_sequences(block, max_q):
 
 
 @pytest.mark.parametrize("new,heads,dim,window", [([1], 2, 64, 0), ([1], 8, 128, 0), ([3], 8, 128, 0), ([8], 8, 128, 0),
-                                                  ([40], 4, 64, 0), ([24], 8, 256, 0), ([1], 4, 128, 9000)])
+                                                  ([40], 4, 64, 0), ([24], 8, 256, 0), ([1], 4, 128, 9000),
+                                                  ([12], 2, 64, 3000), ([300], 2, 128, 2500), ([90], 1, 256, 1000)])
 def test_long_contexts_are_split_and_joined(block, new, heads, dim, window):
     say("attn long", new, heads, dim)
     cache, table, q_start, kv_len, gen = make_batch(block, new, [30000], 64, 1, dim, BF, 2)
