@@ -211,14 +211,15 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
             // A value that only some rows see may be an infinity or a NaN, which
             // a zero weight does not silence in a product: it is left out of
             // the product and added to the rows that see it.
+            FiniteCheck<T> check;
 #pragma unroll
             for (int h = 0; h < HALF; ++h)
 #pragma unroll
                 for (int p = 0; p < 8; ++p)
 #pragma unroll
                     for (int e = 0; e < VEC / 2; ++e)
-                        poisoned |= not_finite<T>(vr[h][p][e]);
-            poisoned = __any(poisoned);
+                        check.add(vr[h][p][e]);
+            poisoned = __any(check.fails());
             if (poisoned)
 #pragma unroll
                 for (int h = 0; h < HALF; ++h)

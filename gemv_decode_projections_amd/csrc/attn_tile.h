@@ -248,7 +248,7 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
     // not silence in a product: it is left out of the product and added to the
     // rows that see it.
     auto masked_product = [&](const char *v, int h, int p, uint32_t held, const u32x4 (&pf)[2]) {
-        bool poisoned = false;
+        FiniteCheck<T> check;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             u32x4 keep;
@@ -262,13 +262,13 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
                 u32x4 f = value_frag(v, 32 * h + 16 * t, d) & keep;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    poisoned |= not_finite<T>(f[e]);
+                    check.add(f[e]);
                     f[e] = finite_only<T>(f[e]);
                 }
                 acc[d] = T::mfma32(f, pf[t], acc[d]);
             }
         }
-        if (!__any(poisoned))
+        if (!__any(check.fails()))
             return;
 #pragma unroll 1
         for (int j = 0; j < 32; ++j) {

@@ -54,13 +54,18 @@ struct F16 {
     static constexpr uint32_t kExponent = 0x7c00u;
 };
 
-// Whether either of two packed values is an infinity or a NaN.
+// Whether packed values hold an infinity or a NaN: two operations per pair,
+// the largest magnitude bits, and one comparison at the end.
 template <class T>
-__device__ __forceinline__ bool not_finite(uint32_t u)
-{
-    constexpr uint32_t e = T::kExponent;
-    return (u & e) == e || (u & (e << 16)) == (e << 16);
-}
+struct FiniteCheck {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 top = {0, 0};
+    __device__ __forceinline__ void add(uint32_t u)
+    {
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, u & 0x7fff7fffu));
+    }
+    __device__ __forceinline__ bool fails() const { return top.x >= T::kExponent || top.y >= T::kExponent; }
+};
 // Both values with those replaced by zero.
 template <class T>
 __device__ __forceinline__ uint32_t finite_only(uint32_t u)
