@@ -27,6 +27,7 @@ _pages = ctypes.POINTER(ctypes.c_int32)
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 HEAD_DIMS = (64, 128, 256)
+ATTN_ZEROED = 32768        # BLK_ATTN_ZEROED
 EXT_PATH = os.path.join(os.path.dirname(_b.LIB_PATH), "_block.so")
 
 
@@ -225,7 +226,8 @@ class AttnWorkspace:
         _need(head_dim in HEAD_DIMS, "head_dim %d, expected one of %s" % (head_dim, HEAD_DIMS))
         self.head_dim = head_dim
         self.bytes = _lib().blk_attn_workspace_bytes(head_dim)
-        self.buffer = torch.zeros(self.bytes, dtype=torch.uint8, device=device)
+        self.buffer = torch.empty(self.bytes, dtype=torch.uint8, device=device)
+        self.buffer[:ATTN_ZEROED].zero_()
         # Any stream may use it from here on.
         torch.cuda.current_stream(self.buffer.device).synchronize()
         self._ptr, self.index = self.buffer.data_ptr(), self.buffer.device.index

@@ -63,6 +63,7 @@ struct AttnArgs {
 constexpr int kAttnSlotRows = 131072;              // rows of all slots together
 constexpr int kAttnMaxSlots = kAttnSlotRows / 16;
 constexpr size_t kAttnCounterBytes = kAttnMaxSlots * sizeof(uint32_t);
+static_assert(kAttnCounterBytes == BLK_ATTN_ZEROED, "the counters are what a caller zeroes");
 constexpr size_t attn_ws_bytes(int dim) { return kAttnCounterBytes + (size_t)kAttnSlotRows * (dim + 2) * 4; }
 
 // One workgroup's share: rows row0 .. row0 + nrows - 1 of sequence `seq`

@@ -11,7 +11,8 @@ namespace gdp {
 // workgroup joins one row: group g takes kJoinRun consecutive splits of every
 // GROUPS * kJoinRun, and the groups' results meet in LDS, in order. (Joined in
 // the tile kernel by the last of 16 workgroups, splits of 64 rows cost 30 us a
-// level.)
+// level.) Bound by its launch and three dependent reads: 7 us for 808 rows of
+// up to 32 splits each (15 MB), 5 us where next to nothing was split.
 constexpr int kJoinRun = 8;
 
 template <class T, int DIM, int ROWS>

@@ -21,6 +21,14 @@
 // Tiles of K and V fill a ring of LDS by DMA, one tile ahead of the products. A
 // tile row's 16-byte pieces are permuted (by the address that each lane of the
 // DMA reads) so that neither read meets a bank conflict.
+//
+// Measured, BF16, heads of 128: chunks of 1000 and 630 tokens over 17 k
+// positions, 32 heads on 8: 290 us, 760 TFLOP/s, half the rate of a large
+// matrix product. The matrix unit is busy 43 % of the time, the vector unit's
+// exponentials take about as long, and a wave's two kinds of work depend on
+// each other. 16 sequences of up to 8 drafted tokens over 250 k positions, 8
+// heads on 1: 37 us before the join, of which 20 at 6.5 TB/s (part of the cache
+// comes from the last level of cache) and the rest the start and the ends.
 #pragma once
 
 #include <type_traits>

@@ -15,7 +15,11 @@
 // Memory bound at the token counts it is for (16 tokens: 64 operations per
 // weight byte). A workgroup owns RB blocks of 16 rows and 16 NT tokens; its
 // waves split K, each unit of 128 k is one 16-byte load per lane and row
-// block, 1 KB contiguous per wave.
+// block, 1 KB contiguous per wave. Measured, BF16: 2304 x 8192, groups of 128,
+// one token: 5.5 us (9.9 MB at 1.8 TB/s: 144 row blocks fill little over half
+// the card, and the time is a launch, one load's latency and the join of the
+// waves); 8192 x 4096, groups of 64, 32 tokens: 9.5 us, bound by the
+// activations that every workgroup reads from L2.
 #include <limits.h>
 
 #include "block_common.h"

@@ -131,9 +131,10 @@ int blk_pool_compact(blk_pool *pool, int max_moves, int32_t *src, int32_t *dst);
  *       q . K[j]), -inf for a token that sees nothing.
  *   max_q: the largest number of new tokens of one sequence, which picks the
  *       kernel (any value >= 1 gives right results; the true one is fastest).
- *   ws: blk_attn_workspace_bytes(head_dim) bytes, 256-byte aligned, zeroed
- *       before the first use; the kernels leave it ready for the next call.
- *       Calls that can overlap need workspaces of their own.
+ *   ws: blk_attn_workspace_bytes(head_dim) bytes, 256-byte aligned, its first
+ *       BLK_ATTN_ZEROED bytes zero before the first use; the kernels leave
+ *       them so. One workspace serves batches of any size and head_dim up to
+ *       its own; calls that can overlap need workspaces of their own.
  * One launch, or two (none if seqs or tokens is 0).
  */
 typedef struct {
@@ -149,6 +150,8 @@ typedef struct {
     int window;     /* 0: none */
     float scale;    /* > 0 */
 } blk_attn_args;
+
+#define BLK_ATTN_ZEROED 32768
 
 int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_args *args, void *ws, size_t ws_bytes,
                  void *stream);

@@ -44,6 +44,11 @@ def test_every_declared_function_is_exported(lib):
         assert hasattr(lib, n), n
 
 
+def test_zeroed_bytes_match_the_header(block):
+    with open(os.path.join(ROOT, "include", "block.h")) as f:
+        assert int(re.search(r"#define BLK_ATTN_ZEROED (\d+)", f.read()).group(1)) == block.ATTN_ZEROED
+
+
 def test_new_statuses_have_texts(lib):
     for s in (-10, -11):
         assert binding.proj_strerror(s) != "unknown status" and s in binding.STATUS

@@ -374,9 +374,11 @@ def test_fork_write_and_compact_keep_what_sequences_read(block):
 
 
 def test_workspace_serves_batches_in_turn(block):
-    # One workspace under kernels of every kind, in turn, gives what fresh ones give.
+    # One workspace under kernels of every kind, in turn, gives what fresh ones give; past its first
+    # bytes it may hold anything.
     say("workspace reuse")
     ws = block.AttnWorkspace(128)
+    ws.buffer[block.ATTN_ZEROED:].fill_(255)
     cases = []
     for i, (new, cached, heads) in enumerate([([1], [6000], 8), ([2, 3], [900, 4000], 8), ([8], [3000], 8), ([50], [2000], 4),
                                               ([1] * 20, [700] * 20, 4)]):
