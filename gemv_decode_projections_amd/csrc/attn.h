@@ -137,7 +137,7 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, 
 //     part as long as a tile has no more than 16 parts and half the places are
 //     taken (one token over 131072 positions: 256 parts 20.5 us, 512 parts 24);
 //   - tile kernels, with more tiles than half the places: the join of 128 rows
-//     costs more than an uneven round, so C is twice that (440 tiles: 288 us,
+//     costs more than an uneven round, so C is twice that (416 tiles: 288 us,
 //     cut for 512 places 446; 256 tiles cut in two: 177 us, whole 203).
 template <int ROWS>
 struct Partition {
@@ -265,12 +265,12 @@ struct Partition {
 
 // The workgroup's unit; false for workgroups past the last one. Workgroups are
 // dealt to the 8 XCDs round-robin; the units are given to the XCDs in
-// contiguous eighths, ordered so that the row tiles that read the same keys
-// follow each other and share an L2, then the heads that lie next to each
+// contiguous eighths. The heads of a key come first, as they lie next to each
 // other in a page (with the heads apart in time 32 sequences x 8 heads took
-// 145 us instead of 131).
+// 145 us instead of 131), then the row tiles, which share their keys in an L2
+// (chunks of 1000 and 630 tokens: 282 us, tiles before heads 289).
 template <int ROWS>
-__device__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
+__device__ __forceinline__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
 {
     Partition<ROWS> part(a);
     auto units = [](const Partition<ROWS> &p) { return p.units(); };
@@ -281,13 +281,14 @@ __device__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
         return false;
     int tiles;
     const int local = part.find(want, units, u, tiles);
-    int tile = 0, rest = local;
+    const int rest = a.by_heads(local);
+    u.kvh = local - rest * a.kv_heads;
+    int tile = 0;
+    u.split = rest;
     if (tiles > 1) {
-        rest = local / tiles;
-        tile = local - rest * tiles;
+        u.split = rest / tiles;
+        tile = rest - u.split * tiles;
     }
-    u.split = a.by_heads(rest);
-    u.kvh = rest - u.split * a.kv_heads;
     u.slot0 += (u.kvh * tiles + tile) * u.splits;
     // Offsets that do not ascend could ask for more slots than there are.
     if (u.splits > 1 && (unsigned)(u.slot0 + u.splits) > (unsigned)kAttnSlotRows / ROWS)

@@ -23,7 +23,7 @@
 // DMA reads) so that neither read meets a bank conflict.
 //
 // Measured, BF16, heads of 128: chunks of 1000 and 630 tokens over 17 k
-// positions, 32 heads on 8: 290 us, 760 TFLOP/s, half the rate of a large
+// positions, 32 heads on 8: 282 us, 780 TFLOP/s, half the rate of a large
 // matrix product. The matrix unit is busy 43 % of the time, the vector unit's
 // exponentials take about as long, and a wave's two kinds of work depend on
 // each other. 16 sequences of up to 8 drafted tokens over 250 k positions, 8
@@ -149,7 +149,8 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
             dma_rows(a.v + off[n], sub_off + 16 * value_piece<DIM>(row + sub, piece), lds_of(s_v[stage.value]) + row * ROWB);
         }
     };
-    auto barrier = [] { asm volatile("s_barrier" ::: "memory"); };
+    // (this wave's reads of LDS have ended: another's DMA overwrites what they read)
+    auto barrier = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
     f32x16 acc[DB];
 #pragma unroll
