@@ -268,7 +268,8 @@ struct Partition {
 // contiguous eighths. The heads of a key come first, as they lie next to each
 // other in a page (with the heads apart in time 32 sequences x 8 heads took
 // 145 us instead of 131), then the row tiles, which share their keys in an L2
-// (chunks of 1000 and 630 tokens: 282 us, tiles before heads 289).
+// (chunks of 1000 and 630 tokens: 282 us, though the L2s fetch 545 MB; tiles
+// before heads 289 and 119 MB).
 template <int ROWS>
 __device__ __forceinline__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
 {
