@@ -378,10 +378,15 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
     for (int stride = 1, level = 0;; stride *= kJoin, ++level) {
         const int first = u.split / (stride * kJoin) * (stride * kJoin);
         const int members = min(kJoin, (u.splits - first + stride - 1) / stride);
+        // Alone at its level (257 splits: the last one, of the second level): the
+        // slot stays as it is, and there is nothing to count.
+        if (members == 1)
+            continue;
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         if (threadIdx.x == 0) {
-            // Counters of the levels lie at slots of different remainders.
+            // Counters of the levels lie at slots of different remainders, and
+            // among the tile's own: two members are more than `level` slots apart.
             uint32_t *c = a.counters + u.slot0 + first + level;
             const uint32_t before = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             const bool last = before == (uint32_t)(members - 1);

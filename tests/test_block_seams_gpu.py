@@ -114,3 +114,14 @@ def test_every_kernel_counts_a_mixed_batch(block, dim, max_q):
     # max_q picks the kernel (16, 32, 64 and 128 rows per tile); any batch is right in each.
     say("seams mixed", dim, max_q)
     check_counts(block, [1, 17, 4], [9001, 3000, 640], 8, 1, dim, FH, 32, 0, max_q)
+
+
+@pytest.mark.parametrize("new,total,heads,kv_heads,dim", [([1, 1], [164000, 2000], 8, 1, 128), ([1], [164000], 4, 2, 64)])
+def test_a_split_alone_at_its_level_touches_no_other_tile(block, new, total, heads, kv_heads, dim):
+    # 257 splits: the last one has no partner in the first two levels of joins. The counters of the
+    # tile behind it are that tile's alone, and all are zero again afterwards.
+    say("seams 257", new, total, heads, kv_heads, dim)
+    ws = block.AttnWorkspace(dim)
+    for _ in range(3):
+        check_counts(block, new, total, heads, kv_heads, dim, FH, 64, ws=ws, codes=(1,))
+        assert not bool(ws.buffer[:block.ATTN_ZEROED].any())
