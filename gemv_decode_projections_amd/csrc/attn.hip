@@ -124,7 +124,7 @@ int check_batch(const blk_batch *b)
 {
     if (!b)
         return PROJ_ERR_NULL;
-    if (b->seqs < 0 || b->tokens < 0 || b->table_width < 1 || b->table_stride < b->table_width)
+    if (b->seqs < 0 || b->tokens < 0 || b->table_width < 1 || (b->table_stride && b->table_stride < b->table_width))
         return PROJ_ERR_ARG;
     if (b->seqs && b->tokens && (!b->q_start || !b->kv_len || !b->table))
         return PROJ_ERR_NULL;

@@ -112,7 +112,7 @@ blk_batch batch_of(PyObject *otable, PyObject *ostart, PyObject *olen, int64_t t
     b.q_start = static_cast<const int32_t *>(pointer(start));
     b.kv_len = static_cast<const int32_t *>(pointer(len));
     b.table = static_cast<const int32_t *>(pointer(table));
-    b.table_stride = std::max(table.stride(0), width);
+    b.table_stride = seqs > 1 ? table.stride(0) : width;       // (one row's may be anything)
     b.table_width = (int)width;
     b.seqs = (int)seqs;
     b.tokens = (int)tokens;

@@ -57,7 +57,8 @@ typedef struct {
  * the new ones included, so new token i of n stands at position
  * kv_len[b] - n + i. Position p is in page table[b * table_stride + p /
  * page_size]; a table entry outside 0 .. n_pages - 1 holds no tokens (a page
- * already given back, say, outside an attention window).
+ * already given back, say, outside an attention window). A table_stride of 0
+ * gives all sequences one row; otherwise rows do not overlap (PROJ_ERR_ARG).
  * All three arrays are int32 on the device. Values are bounded where they
  * are read: kv_len to 0 .. table_width * page_size, q_start to 0 .. tokens.
  */

@@ -1,0 +1,82 @@
+"""GPU tests of the tensors that a caller may hand to the block operators: views whose strides say
+something unusual, or nothing."""
+
+import math
+
+import pytest
+import torch
+
+from gemv_decode_projections_amd.binding import ProjError
+
+pytestmark = pytest.mark.gpu
+
+BF, FH = torch.bfloat16, torch.float16
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def block():
+    from gemv_decode_projections_amd import block as b
+
+    return b
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def filled(block, pages, page, kv_heads, dim, seed=0):
+    gen = torch.Generator(DEV).manual_seed(seed)
+    shape = (pages, page, kv_heads, dim)
+    return block.KvCache(*(torch.randn(shape, generator=gen, device=DEV).to(BF) for _ in range(2))), gen
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_one_table_row_for_several_sequences(block, max_q):
+    # An expanded row has a stride of 0; what lies behind its storage are valid page numbers, of others.
+    say("expanded table", max_q)
+    cache, gen = filled(block, 32, 16, 2, 64)
+    store = ints(list(range(31, 0, -1)) * 4)
+    row, seqs = store[:6][None], 4
+    q_start, kv_len = ints([0, 1, 2, 5, 6]), ints([90, 17, 96, 50])
+    q = torch.randn(6, 4, 64, generator=gen, device=DEV).to(BF)
+    outs = []
+    for table in (row.expand(seqs, -1), row.repeat(seqs, 1)):
+        out = torch.full_like(q, math.nan)
+        block.attn_run(q, cache, table, q_start, kv_len, out, block.AttnWorkspace(64), max_q=max_q)
+        torch.cuda.synchronize()
+        outs.append(out)
+    assert torch.equal(*outs)
+    kv = torch.randn(2, 3, 2, 64, generator=gen, device=DEV).to(BF)
+    caches = []
+    for table in (row.expand(2, -1), row.repeat(2, 1)):         # one appends to the first page, one to the fifth
+        c = block.KvCache(cache.k.clone(), cache.v.clone())
+        block.kv_append(kv[0], kv[1], c, table, ints([0, 2, 3]), ints([9, 70]))
+        torch.cuda.synchronize()
+        caches.append(c)
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+    assert torch.equal(caches[0].k[31, 7], kv[0, 0]) and torch.equal(caches[0].v[27, 5], kv[1, 2])
+    overlapping = store.as_strided((seqs, 6), (3, 1))
+    with pytest.raises(ProjError, match="ARG"):
+        block.attn_run(q, cache, overlapping, q_start, kv_len, out, block.AttnWorkspace(64), max_q=max_q)
+    with pytest.raises(ProjError, match="ARG"):
+        block.kv_append(kv[0], kv[1], cache, overlapping[:2], ints([0, 2, 3]), ints([9, 70]))
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_a_single_table_row_of_any_stride(block, max_q):
+    say("single table row", max_q)
+    cache, gen = filled(block, 16, 16, 1, 64)
+    q = torch.randn(2, 4, 64, generator=gen, device=DEV).to(BF)
+    row = [5, 3, 9, 1]
+    outs = []
+    for table in (ints([row]), ints(row)[:, None].t(), ints([row]).as_strided((1, 4), (0, 1))):
+        out = torch.full_like(q, math.nan)
+        block.attn_run(q, cache, table, ints([0, 2]), ints([60]), out, block.AttnWorkspace(64), max_q=max_q)
+        torch.cuda.synchronize()
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
