@@ -100,16 +100,15 @@ __device__ __forceinline__ I wave_scan(I x)
     x += lane_moved<0x143, 0xc>(x);
     return x;
 }
-// The largest of the lanes' values, none negative.
-__device__ __forceinline__ int wave_max(int x)
+// Inclusive maxima over the wave's lanes, no value negative.
+__device__ __forceinline__ int wave_max_scan(int x)
 {
     x = max(x, lane_moved<0x111, 0xf>(x));
     x = max(x, lane_moved<0x112, 0xf>(x));
     x = max(x, lane_moved<0x114, 0xf>(x));
     x = max(x, lane_moved<0x118, 0xf>(x));
     x = max(x, lane_moved<0x142, 0xa>(x));
-    x = max(x, lane_moved<0x143, 0xc>(x));
-    return __builtin_amdgcn_readlane(x, kWave - 1);
+    return max(x, lane_moved<0x143, 0xc>(x));
 }
 __device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, kWave - 1); }
 
@@ -139,6 +138,8 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, 
 //   - tile kernels, with more tiles than half the places: the join of 128 rows
 //     costs more than an uneven round, so C is twice that (416 tiles: 288 us,
 //     cut for 512 places 446; 256 tiles cut in two: 177 us, whole 203).
+// (All of it inlined: called as functions, a unit's fields come back through
+// memory and are no longer scalars.)
 template <int ROWS>
 struct Partition {
     struct Shape {
@@ -148,32 +149,40 @@ struct Partition {
     Shape s;             // the lane's sequence of the last 64 looked at
     int c;
     float per_c;
+    int before;          // where the next 64 sequences begin at the earliest
 
-    __device__ void shape(int b)
+    // The shapes of sequences b0 .. b0 + 63, in turn from 0. An offset counts as
+    // the largest up to it: sequences do not overlap then, and their rows stay
+    // within what the grid and the slots were made for.
+    __device__ __forceinline__ void shape(int b0)
     {
+        const int b = b0 + (int)(threadIdx.x % kWave);
         s = Shape{0, 0, 0, 0, 0, 0, 1};
-        if (b < a.seqs) {
+        if (b < a.seqs)
             seq_bounds(a, b, s.tok0, s.n, s.len);
-            s.tiles = (s.n * a.group + ROWS - 1) / ROWS;
-            if (a.window > 0)
-                s.first = max(0, s.len - s.n - a.window + 1) & -a.kv_step;
-            s.range = s.len - s.first;
-        }
+        const int end = s.tok0 + s.n, from = max(b0 ? before : 0, wave_max_scan(s.tok0));
+        s.tok0 = from;
+        s.n = max(end - from, 0);
+        before = last_lane(from + s.n);
+        s.tiles = (s.n * a.group + ROWS - 1) / ROWS;
+        if (a.window > 0)
+            s.first = max(0, s.len - s.n - a.window + 1) & -a.kv_step;
+        s.range = s.len - s.first;
     }
     // ceil(range / c): the FP32 quotient is at most one off.
-    __device__ void cut()
+    __device__ __forceinline__ void cut()
     {
         int q = (int)((float)(s.range + c - 1) * per_c);
         q += q * c < s.range ? 1 : 0;
         q -= (q - 1) * c >= s.range ? 1 : 0;
         s.splits = max(q, 1);
     }
-    __device__ explicit Partition(const AttnArgs &args) : a(args)
+    __device__ __forceinline__ explicit Partition(const AttnArgs &args) : a(args)
     {
         unsigned long long w = 0;
         int t = 0, longest = 0;
         for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
-            shape(b0 + (int)(threadIdx.x % kWave));
+            shape(b0);
             w += (unsigned long long)s.tiles * (unsigned)s.range;
             t += s.tiles;
             longest = max(longest, s.range);
@@ -188,7 +197,7 @@ struct Partition {
         if (ROWS <= 32) {
             fit = fit && per < 2048.f;
             set_part(fmaxf(fit ? per : per / (float)a.rounds,
-                           fminf(512.f, fmaxf((float)wave_max(longest) * (1.f / 16), all * a.per_target * 2.f))));
+                           fminf(512.f, fmaxf((float)last_lane(wave_max_scan(longest)) * (1.f / 16), all * a.per_target * 2.f))));
         } else {
             set_part(fit ? per : 2.f * per);
         }
@@ -200,29 +209,29 @@ struct Partition {
                 set_part((float)c * (float)n * a.per_target);
             }
     }
-    __device__ void set_part(float positions)
+    __device__ __forceinline__ void set_part(float positions)
     {
         const int p = (int)fminf(positions + 1.0f, 0x1p29f);
         c = __builtin_amdgcn_readfirstlane(max(a.min_split, (p + a.kv_step - 1) & -a.kv_step));
         per_c = 1.0f / (float)c;
         cut();
     }
-    __device__ int units() const { return s.tiles * s.splits * a.kv_heads; }
-    __device__ int slots() const { return s.splits > 1 ? units() : 0; }
+    __device__ __forceinline__ int units() const { return s.tiles * s.splits * a.kv_heads; }
+    __device__ __forceinline__ int slots() const { return s.splits > 1 ? units() : 0; }
     // Blocks of rows whose splits have to be joined (join_rows each, attn_join.h).
-    __device__ int joins(int few, int rows) const
+    __device__ __forceinline__ int joins(int few, int rows) const
     {
         const int per = s.splits <= few ? rows : 1;
         return s.splits > 1 ? (s.n * a.group + per - 1) / per * a.kv_heads : 0;
     }
 
     template <class Count>
-    __device__ int total(Count count)
+    __device__ __forceinline__ int total(Count count)
     {
         int t = 0;
         for (int b0 = 0; b0 < a.seqs; b0 += kWave) {
             if (a.seqs > kWave) {
-                shape(b0 + (int)(threadIdx.x % kWave));
+                shape(b0);
                 cut();
             }
             t += count(*this);
@@ -233,12 +242,12 @@ struct Partition {
     // sequence: sets u's sequence and its first slot, returns the item's
     // number inside the sequence.
     template <class Count>
-    __device__ int find(int want, Count count, AttnUnit &u, int &tiles)
+    __device__ __forceinline__ int find(int want, Count count, AttnUnit &u, int &tiles)
     {
         int items_before = 0, slots_before = 0;
         for (int b0 = 0;; b0 += kWave) {
             if (a.seqs > kWave) {
-                shape(b0 + (int)(threadIdx.x % kWave));
+                shape(b0);
                 cut();
             }
             const int isum = items_before + wave_scan(count(*this));
@@ -291,7 +300,7 @@ __device__ __forceinline__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u
         tile = rest - u.split * tiles;
     }
     u.slot0 += (u.kvh * tiles + tile) * u.splits;
-    // Offsets that do not ascend could ask for more slots than there are.
+    // (never more than there are, see kAttnSlotRows; a slot past them is no memory)
     if (u.splits > 1 && (unsigned)(u.slot0 + u.splits) > (unsigned)kAttnSlotRows / ROWS)
         return false;
     u.row0 = tile * ROWS;

@@ -61,6 +61,9 @@ typedef struct {
  * gives all sequences one row; otherwise rows do not overlap (PROJ_ERR_ARG).
  * All three arrays are int32 on the device. Values are bounded where they
  * are read: kv_len to 0 .. table_width * page_size, q_start to 0 .. tokens.
+ * q_start does not descend; if it does, it is unspecified whose new tokens
+ * are whose, but not that they are within the tensors. Rows of no sequence
+ * (before q_start[0], from q_start[seqs] on) are neither read nor written.
  */
 typedef struct {
     const int32_t *q_start;     /* seqs + 1 */

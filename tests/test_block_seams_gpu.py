@@ -125,3 +125,28 @@ def test_a_split_alone_at_its_level_touches_no_other_tile(block, new, total, hea
     for _ in range(3):
         check_counts(block, new, total, heads, kv_heads, dim, FH, 64, ws=ws, codes=(1,))
         assert not bool(ws.buffer[:block.ATTN_ZEROED].any())
+
+
+@pytest.mark.parametrize("max_q,heads", [(2, 8), (1, 4), (3, 8), (8, 8), (40, 4)])
+@pytest.mark.parametrize("seqs", [6, 130])
+def test_offsets_that_descend_leave_the_workspace_usable(block, seqs, max_q, heads):
+    # Sequences that would overlap: more rows than there are tokens. Every counter of the workspace is
+    # zero again, rows are written whole or not at all, and a valid batch on it is right.
+    say("descending offsets", seqs, max_q, heads)
+    tokens, dim = 16, 128
+    total = [1000 + 13 * (b % 7) for b in range(seqs)]
+    cache, table = counting_batch(block, total, 64, 1, dim, BF, 0, 2)
+    kv_len = torch.tensor(total, dtype=torch.int32, device=DEV)
+    ws = block.AttnWorkspace(dim)
+    q = torch.randn(tokens, heads, dim, device=DEV).to(BF)
+    rng = random.Random(seqs)
+    for start in ([0, tokens] * seqs, [tokens, 0] * seqs, [rng.randint(-3, tokens + 3) for _ in range(seqs + 1)],
+                  [7, 2 ** 31 - 1, -(2 ** 31)] * seqs):
+        q_start = torch.tensor(start[:seqs + 1], dtype=torch.int32, device=DEV)
+        out = torch.full_like(q, math.nan)
+        block.attn_run(q, cache, table, q_start, kv_len, out, ws, max_q=max_q)
+        torch.cuda.synchronize()
+        assert not bool(ws.buffer[:block.ATTN_ZEROED].any())
+        gone = torch.isnan(out).all(-1)
+        assert bool((torch.isnan(out).any(-1) == gone).all())
+    check_counts(block, [max_q, 1], [9000, 300], heads, 1, dim, FH, 64, ws=ws)
