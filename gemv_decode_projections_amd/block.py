@@ -10,7 +10,8 @@ library, on the stream given or torch's current one. Calls launch and return;
 nothing is allocated, synchronized or copied to the host. The run functions'
 checks are compiled (csrc/block_py.cpp): a tensor of the wrong shape, type,
 device or layout raises ValueError before anything is launched, what the
-library itself refuses raises ProjError.
+library itself refuses raises ProjError (PROJ_ERR_DEVICE: the tensors are on
+one GPU, and another is current).
 """
 
 import ctypes
@@ -33,11 +34,13 @@ EXT_PATH = os.path.join(os.path.dirname(_b.LIB_PATH), "_block.so")
 
 class _Cache(ctypes.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("page_stride", _i64), ("token_stride", _i64), ("head_stride", _i64),
-                ("n_pages", _i), ("page_size", _i), ("kv_heads", _i), ("head_dim", _i), ("dtype", _i)]
+                ("n_pages", _i), ("page_size", _i), ("kv_heads", _i), ("head_dim", _i), ("dtype", _i),
+                ("_end", _i), ("device", _i)]        # (behind blk_cache: the GPU, for the compiled checks)
 
 
 class _W4(ctypes.Structure):
-    _fields_ = [("n", _i), ("k", _i), ("group", _i), ("dtype", _i), ("has_zeros", _i)]
+    _fields_ = [("n", _i), ("k", _i), ("group", _i), ("dtype", _i), ("has_zeros", _i),
+                ("device", _i)]                      # (behind blk_w4)
 
 
 _LIB = None
@@ -87,7 +90,10 @@ def _ext():
 def _raw_stream(stream, index):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    _need(stream.device_index == index, "the stream is of GPU %d, the tensors are on GPU %d" % (stream.device_index, index))
+    return stream.cuda_stream
 
 
 def _fail(rc, what):
@@ -120,7 +126,8 @@ class KvCache:
         self.n_pages, self.page_size, self.kv_heads, self.head_dim = pages, size, heads, dim
         self.dtype, self.device = k.dtype, k.device
         s = k.stride()
-        self._c = _Cache(k.data_ptr(), v.data_ptr(), s[0], s[1], s[2], pages, size, heads, dim, DTYPES[k.dtype])
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), s[0], s[1], s[2], pages, size, heads, dim, DTYPES[k.dtype],
+                         0, k.device.index)
         self._addr, self._index = ctypes.addressof(self._c), k.device.index
 
     @classmethod
@@ -275,11 +282,12 @@ def w4_prepare(q, scales, zeros=None, group=128):
           and scales.device == q.device, "scales must be a contiguous bfloat16 or float16 tensor %d x %d" % (n, k // group))
     _need(zeros is None or (zeros.dtype == torch.uint8 and zeros.shape == scales.shape and zeros.is_contiguous()
                             and zeros.device == q.device), "zeros must be a contiguous uint8 tensor %d x %d" % (n, k // group))
-    shape = _W4(n, k, group, DTYPES[scales.dtype], int(zeros is not None))
+    shape = _W4(n, k, group, DTYPES[scales.dtype], int(zeros is not None), q.device.index)
     packed = torch.empty(_lib().blk_w4_packed_bytes(shape), dtype=torch.uint8, device=q.device)
     stream = torch.cuda.current_stream(q.device)
-    _fail(_lib().blk_w4_pack(shape, q.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
-                             packed.data_ptr(), stream.cuda_stream), "w4_prepare")
+    with torch.cuda.device(q.device):
+        _fail(_lib().blk_w4_pack(shape, q.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
+                                 packed.data_ptr(), stream.cuda_stream), "w4_prepare")
     stream.synchronize()
     return W4Weight(shape, packed, scales.dtype)
 

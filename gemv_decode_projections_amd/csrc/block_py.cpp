@@ -7,8 +7,12 @@
 // tensor that the operator does not take, and returns the library's status.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cmath>
+#include <cstddef>
 #include <string>
 #include <vector>
 
@@ -16,6 +20,17 @@
 #include "../../include/proj.h"
 
 namespace {
+
+// What block.py hands over: the C structure, and the GPU that its memory is on.
+struct PyCache {
+    blk_cache c;
+    int device;
+};
+struct PyW4 {
+    blk_w4 w;
+    int device;
+};
+static_assert(offsetof(PyCache, device) == 64 && offsetof(PyW4, device) == 20, "block.py's _Cache and _W4");
 
 struct Refused {
     std::string what;
@@ -65,6 +80,11 @@ const T *address(PyObject *o)
         throw Refused{"not an address"};
     return static_cast<const T *>(p);
 }
+
+at::Device gpu(int index) { return at::Device(at::kCUDA, (c10::DeviceIndex)index); }
+
+// Launches go to the current device, whichever the stream's: it has to be the tensors'.
+bool is_current(const at::Device &dev) { return c10::impl::VirtualGuardImpl(at::kCUDA).getDevice() == dev; }
 
 void *raw(PyObject *o) { return PyLong_AsVoidPtr(o); }
 
@@ -161,13 +181,14 @@ PyObject *entry(Py_ssize_t got, Py_ssize_t want, F f)
 PyObject *attn_run(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return entry(n, 14, [&] {
-        const blk_cache &c = *address<blk_cache>(a[0]);
+        const PyCache &cache = *address<PyCache>(a[0]);
+        const blk_cache &c = cache.c;
         const at::Tensor &q = tensor(a[3], "q"), &out = tensor(a[7], "out");
         need(q.dim() == 3, "q must be tokens x heads x head_dim");
         const int64_t tokens = q.size(0), heads = q.size(1);
         if (heads < 1 || heads % c.kv_heads)
             throw Refused{"q has " + std::to_string(heads) + " heads, the cache " + std::to_string(c.kv_heads)};
-        const at::Device dev = q.device();
+        const at::Device dev = gpu(cache.device);
         blk_attn_args x{};
         heads_of(q, "q", c, tokens, heads, dev, x.q_stride, x.q_head_stride);
         heads_of(out, "out", c, tokens, heads, dev, x.out_stride, x.out_head_stride);
@@ -180,7 +201,7 @@ PyObject *attn_run(PyObject *, PyObject *const *a, Py_ssize_t n)
             const at::Tensor &lse = tensor(a[9], "lse");
             need(lse.scalar_type() == at::kFloat && lse.dim() == 2 && lse.size(0) == tokens && lse.size(1) == heads &&
                      lse.is_contiguous() && lse.device() == dev,
-                 "lse must be a contiguous float32 tensor tokens x heads on q's device");
+                 "lse must be a contiguous float32 tensor tokens x heads on the cache's device");
             x.lse = static_cast<float *>(pointer(lse));
         }
         x.q = pointer(q);
@@ -190,6 +211,8 @@ PyObject *attn_run(PyObject *, PyObject *const *a, Py_ssize_t n)
         x.scale = a[11] == Py_None ? 1.0f / std::sqrt((float)c.head_dim) : (float)real_of(a[11], "scale");
         x.window = int_of(a[12], "window");
         const blk_batch b = batch_of(a[4], a[5], a[6], tokens, dev);
+        if (!is_current(dev))
+            return (int)PROJ_ERR_DEVICE;
         return blk_attn_run(&c, &b, &x, raw(a[1]), PyLong_AsSize_t(a[2]), raw(a[13]));
     });
 }
@@ -198,15 +221,18 @@ PyObject *attn_run(PyObject *, PyObject *const *a, Py_ssize_t n)
 PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return entry(n, 7, [&] {
-        const blk_cache &c = *address<blk_cache>(a[0]);
+        const PyCache &cache = *address<PyCache>(a[0]);
+        const blk_cache &c = cache.c;
         const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
         need(k.dim() == 3, "k must be tokens x kv_heads x head_dim");
-        const at::Device dev = k.device();
+        const at::Device dev = gpu(cache.device);
         int64_t ks, kh, vs, vh;
         heads_of(k, "k", c, k.size(0), c.kv_heads, dev, ks, kh);
         heads_of(v, "v", c, k.size(0), c.kv_heads, dev, vs, vh);
         need(ks == vs && (kh == vh || c.kv_heads == 1), "k and v have different strides");
         const blk_batch b = batch_of(a[3], a[4], a[5], k.size(0), dev);
+        if (!is_current(dev))
+            return (int)PROJ_ERR_DEVICE;
         return blk_kv_append(&c, &b, pointer(k), pointer(v), ks, kh, raw(a[6]));
     });
 }
@@ -215,7 +241,8 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
 PyObject *kv_copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return entry(n, 4, [&] {
-        const blk_cache &c = *address<blk_cache>(a[0]);
+        const PyCache &cache = *address<PyCache>(a[0]);
+        const blk_cache &c = cache.c;
         std::vector<int32_t> pages[2];
         for (int i = 0; i < 2; ++i) {
             PyObject *seq = PySequence_Fast(a[1 + i], "");
@@ -239,6 +266,8 @@ PyObject *kv_copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (pages[0].size() != pages[1].size())
             throw Refused{std::to_string(pages[0].size()) + " source pages, " + std::to_string(pages[1].size()) + " destinations"};
         need(pages[0].size() <= INT32_MAX, "too many pages");
+        if (!is_current(gpu(cache.device)))
+            return (int)PROJ_ERR_DEVICE;
         return blk_kv_copy_pages(&c, pages[0].data(), pages[1].data(), (int)pages[0].size(), raw(a[3]));
     });
 }
@@ -247,12 +276,16 @@ PyObject *kv_copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n)
 PyObject *w4_run(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return entry(n, 5, [&] {
-        const blk_w4 &w = *address<blk_w4>(a[0]);
+        const PyW4 &weight = *address<PyW4>(a[0]);
+        const blk_w4 &w = weight.w;
+        const at::Device dev = gpu(weight.device);
         const at::Tensor &x = tensor(a[2], "x"), &out = tensor(a[3], "out");
         need(x.dim() == 2, "x must be m x k");
-        const int64_t m = x.size(0), xs = rows_of(x, "x", m, w.k, w.dtype, x.device());
-        const int64_t os = rows_of(out, "out", m, w.n, w.dtype, x.device());
+        const int64_t m = x.size(0), xs = rows_of(x, "x", m, w.k, w.dtype, dev);
+        const int64_t os = rows_of(out, "out", m, w.n, w.dtype, dev);
         need(m <= INT32_MAX, "too many rows");
+        if (!is_current(dev))
+            return (int)PROJ_ERR_DEVICE;
         return blk_w4_run(&w, raw(a[1]), pointer(x), xs, (int)m, pointer(out), os, raw(a[4]));
     });
 }
@@ -308,6 +341,8 @@ PyObject *norm_run(PyObject *, PyObject *const *a, Py_ssize_t n)
                 }
             }
         }
+        if (!is_current(dev))
+            return (int)PROJ_ERR_DEVICE;
         return blk_norm_run(&x, (int)m, raw(a[9]));
     });
 }

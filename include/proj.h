@@ -56,7 +56,7 @@ enum proj_status {
     PROJ_ERR_NOT_PREPARED = -5, /* proj_run before proj_prepare for that layer */
     PROJ_ERR_UNSUPPORTED = -6,  /* a requested kernel configuration is not built */
     PROJ_ERR_HIP = -7,          /* a HIP runtime call failed (see proj_last_hip_error) */
-    PROJ_ERR_DEVICE = -8,       /* current device differs from the one the layer was prepared on */
+    PROJ_ERR_DEVICE = -8,       /* current device differs from the one the layer was prepared (or the tensors are) on */
     PROJ_ERR_SCRATCH = -9,      /* proj_run_noalloc: the plan needs more split-K scratch than it has */
     PROJ_ERR_ARG = -10,         /* block.h: a size, stride, type or index outside what the operator takes */
     PROJ_ERR_PAGES = -11        /* block.h: the page pool has too few free pages */

@@ -80,3 +80,36 @@ def test_a_single_table_row_of_any_stride(block, max_q):
         torch.cuda.synchronize()
         outs.append(out)
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_another_gpu_than_the_cache_or_the_weight(block):
+    # A cache and a weight that say they are on the next GPU: tensors of this one are refused, and so is
+    # a call without tensors while this one is current.
+    say("devices")
+    here = torch.cuda.current_device()
+    cache, _ = filled(block, 4, 16, 1, 64)
+    w = block.w4_prepare(torch.zeros(8, 32, dtype=torch.uint8, device=DEV), torch.zeros(8, 2, dtype=BF, device=DEV), group=32)
+    q = torch.zeros(1, 2, 64, dtype=BF, device=DEV)
+    x, out = torch.zeros(1, 64, dtype=BF, device=DEV), torch.zeros(1, 8, dtype=BF, device=DEV)
+    table, q_start, kv_len, ws = ints([[0]]), ints([0, 1]), ints([1]), block.AttnWorkspace(64)
+    cache._c.device = w._shape.device = here + 1
+    with pytest.raises(ValueError, match="device"):
+        block.attn_run(q, cache, table, q_start, kv_len, torch.zeros_like(q), ws, max_q=1)
+    with pytest.raises(ValueError, match="device"):
+        block.kv_append(q[:, :1], q[:, :1], cache, table, q_start, kv_len)
+    with pytest.raises(ProjError, match="DEVICE"):
+        block.kv_copy_pages(cache, [0], [1])
+    with pytest.raises(ValueError, match="cuda:%d" % (here + 1)):
+        block.w4_run(w, x, out)
+    cache._c.device = w._shape.device = here
+    block.attn_run(q, cache, table, q_start, kv_len, torch.zeros_like(q), ws, max_q=1)
+    block.kv_append(q[:, :1], q[:, :1], cache, table, q_start, kv_len)
+    block.kv_copy_pages(cache, [0], [1])
+    block.w4_run(w, x, out)
+
+    class Stream:
+        device_index, cuda_stream = here + 1, 0
+
+    with pytest.raises(ValueError, match="stream"):
+        block.w4_run(w, x, out, stream=Stream())
+    torch.cuda.synchronize()
