@@ -1,16 +1,14 @@
 // Products with 4-bit weights and group scales (include/block.h, blk_w4_*):
 //     out[m, n] = sum over groups g of s[n, g] * sum over k in g of (q[n, k] - z[n, g]) x[m, k].
 //
-// The weights become matrix operands without a conversion instruction: the
-// 16-bit pattern 0x4300 | q is the BF16 number 128 + q (0x6400 | q the FP16
-// number 1024 + q), so two weights take one shift and one and-or. Products are
-// exact, sums FP32, and the scale multiplies the group's FP32 sum, so no
-// weight is ever rounded. The offset comes off
-//   FP16: exactly, by one packed subtraction of 1024 + z before the product;
-//   BF16 (no packed subtraction): from the group's sum, as (128 + z) * sum x,
-//         with sum x from a product with ones, one per 32 k for all rows.
-// The sums then hold up to 136 |sum x| next to the result, which costs about
-// 2^-24 * 136 / 4.6 of it, far below the output's 2^-9.
+// The weights become matrix operands without a conversion instruction: four
+// bits or'ed to the end of an FP16 number are that number plus q units of its
+// last place, z comes off by one packed subtraction, and BF16 takes two more
+// operations on the bits (weight_operand; the conversion of signed nibbles
+// takes longer: 2304 x 8192, one token 7.3 us, this way 6.5). So an operand is
+// q - z itself, exact: an activation meets nothing else, be it an infinity or
+// an outlier on weights of zero. Products are exact, sums FP32, and the scale
+// multiplies the group's FP32 sum, so no weight is ever rounded.
 //
 // Memory bound at the token counts it is for (16 tokens: 64 operations per
 // weight byte). A workgroup owns RB blocks of 16 rows and 16 NT tokens; its
@@ -29,10 +27,19 @@ namespace {
 
 constexpr int kUnitK = 128;            // k per 16-byte load of a lane
 
+// FP16 number with the weight's four bits at its end, and what BF16 operands
+// are scaled by (see weight_operand).
+template <class T>
+constexpr uint32_t w4_magic()
+{
+    return T::kId == BLK_BF16 ? 0x5800u : 0x6400u;
+}
+constexpr float kBf16Scale = 524288.f;
+
 struct W4Args {
     const u32x4 *w;                    // [row block][unit][lane]
     const char *scale;                 // [row block][unit][128 / G][16 rows], 16 bits
-    const char *zero;                  // same shape: 128 + z (1024 + z); nullptr: z = 8
+    const char *zero;                  // same shape: w4_magic + z; nullptr: z = 8
     const char *x;
     char *out;
     int64_t x_stride, out_stride;      // bytes
@@ -40,12 +47,26 @@ struct W4Args {
     int wide_out;                      // output rows take 8-byte stores
 };
 
-// Weight pair j (elements 2j and 2j + 1 of the eight in w) with its offset.
+// The eight weights of w as an operand, q - z in both types (z twice in `z`, as
+// the number that is taken off).
+//   FP16: 1024 + q by a shift and an and-or, less 1024 + z.
+//   BF16 has no packed subtraction: (128 + q / 8) - (128 + z / 8) in FP16. The
+//   exponent of (q - z) / 8, 12 to 15 or 0, has its upper three bits alike
+//   (011) wherever it is not zero: kept in place with the sign, and repeated
+//   above the other two and the significand three bits further down, they make
+//   the BF16 number (q - z) 2^-19, or zero.
 template <class T>
-__device__ __forceinline__ uint32_t weight_pair(uint32_t w, int j)
+__device__ __forceinline__ u32x4 weight_operand(uint32_t w, uint32_t z, uint32_t nibbles)
 {
-    constexpr uint32_t magic = T::kId == BLK_BF16 ? 0x43004300u : 0x64006400u;
-    return ((w >> (4 * j)) & 0x000f000fu) | magic;
+    constexpr uint32_t magic = w4_magic<T>() * 0x10001u;
+    u32x4 f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t q = ((w >> (4 * j)) & nibbles) | magic;
+        const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, q) - __builtin_bit_cast(f16x2, z));
+        f[j] = T::kId == BLK_BF16 ? (h & 0xf000f000u) | (h >> 3 & 0x0fff0fffu) : h;
+    }
+    return f;
 }
 
 // CH units of a wave are loaded at once, weights, scales and activations, all
@@ -94,12 +115,14 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint32_t one = 0x3f803f80u;
-    const u32x4 ones = {one, one, one, one};
+    // (in a vector register, which an and-or can take next to the other constant)
+    uint32_t nibbles = 0x000f000fu;
+    asm volatile("" : "+v"(nibbles));
 
     for (int first = u0; first < u1; first += CH) {
         u32x4 w[CH][RB], xf[CH][NT][4];
-        u32x2 sc[CH][GPU_][RB], zc[CH][GPU_][RB];
+        u32x2 sc[CH][GPU_][RB];
+        uint32_t zc[CH][GPU_][RB];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             // Units past the wave's last load that one again; k past the
@@ -120,13 +143,10 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a)
                 for (int r = 0; r < RB; ++r) {
                     const int64_t group = ((block[r] + u) * GPU_ + g) * 32;
                     sc[c][g][r] = *reinterpret_cast<const u32x2 *>(a.scale + group + quad * 8);
-                    zc[c][g][r] = u32x2{BF ? 0x43084308u : 0x64086408u, 0x43084308u};
-                    if (a.zero) {
-                        if constexpr (BF)
-                            zc[c][g][r] = *reinterpret_cast<const u32x2 *>(a.zero + group + quad * 8);
-                        else
-                            zc[c][g][r].x = *reinterpret_cast<const uint16_t *>(a.zero + group + col * 2) * 0x10001u;
-                    }
+                    // (as loaded: an operation on it here would wait for it)
+                    zc[c][g][r] = w4_magic<T>() | 8u;
+                    if (a.zero)
+                        zc[c][g][r] = *reinterpret_cast<const uint16_t *>(a.zero + group + col * 2);
                 }
         }
 #pragma unroll
@@ -152,48 +172,27 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a)
             for (int g = 0; g < GPU_; ++g) {
                 if ((first + c) * kUnitK + G * g >= a.k)
                     break;
-                f32x4 xs[NT];
-                if constexpr (BF)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        xs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int s = 0; s < SPG; ++s)
-                            xs[t] = T::mfma16(ones, xf[c][t][g * SPG + s], xs[t]);
-                    }
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
                     f32x4 part[NT];
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
                         part[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    const uint32_t zrow = zc[c][g][r].x;
+                    const uint32_t z = __builtin_amdgcn_perm(0u, zc[c][g][r], 0x01000100u);
 #pragma unroll
                     for (int s = 0; s < SPG; ++s) {
-                        u32x4 wf;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t p = weight_pair<T>(w[c][r][g * SPG + s], j);
-                            if constexpr (!BF)
-                                p = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) - __builtin_bit_cast(f16x2, zrow));
-                            wf[j] = p;
-                        }
+                        const u32x4 wf = weight_operand<T>(w[c][r][g * SPG + s], z, nibbles);
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
                             part[t] = T::mfma16(wf, xf[c][t][g * SPG + s], part[t]);
                     }
-                    const u32x2 s2 = sc[c][g][r], z2 = zc[c][g][r];
+                    const u32x2 s2 = sc[c][g][r];
                     const float sf[4] = {T::lo(s2.x), T::hi(s2.x), T::lo(s2.y), T::hi(s2.y)};
-                    const float zf[4] = {T::lo(z2.x), T::hi(z2.x), T::lo(z2.y), T::hi(z2.y)};
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float v = part[t][i];
-                            if constexpr (BF)
-                                v -= zf[i] * xs[t][i];
-                            acc[r][t][i] += sf[i] * v;
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            acc[r][t][i] += sf[i] * part[t][i];
                 }
             }
         }
@@ -211,6 +210,8 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a)
 #pragma unroll
         for (int w = 1; w < WAVES; ++w)
             v += s_part[w][i][lane];
+        if constexpr (BF)
+            v *= kBf16Scale;
         const int tok = tok0 + 16 * t + col;
         const int row = (rb0 + r) * 16 + 4 * quad;
         if (tok >= a.m || row >= a.n)
@@ -269,9 +270,8 @@ __global__ void w4_pack_scales_kernel(const uint16_t *scales, const uint8_t *zer
     const bool in = row < n && g < groups;
     dscale[id] = in ? scales[(int64_t)row * groups + g] : 0;
     if (zeros) {
-        // 128 + z in BF16, 1024 + z in FP16: z of one byte, 0..15.
-        const uint32_t z = in ? zeros[(int64_t)row * groups + g] & 15u : 8u;
-        dzero[id] = (uint16_t)((T::kId == BLK_BF16 ? 0x4300u : 0x6400u) | z);
+        // z of one byte, 0..15.
+        dzero[id] = (uint16_t)(w4_magic<T>() | (in ? zeros[(int64_t)row * groups + g] & 15u : 8u));
     }
 }
 
