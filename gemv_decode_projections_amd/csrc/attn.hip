@@ -113,9 +113,10 @@ int check_cache(const blk_cache *c)
     if (c->n_pages < 1 || c->kv_heads < 1 || c->kv_heads > 65535 || c->page_size < 8 ||
         (c->page_size & (c->page_size - 1)))
         return PROJ_ERR_ARG;
-    if (!stride_ok(c->page_stride) || !stride_ok(c->token_stride) || !stride_ok(c->head_stride) ||
-        c->page_stride >= kMaxOffset || c->token_stride >= kMaxOffset / 2 || c->head_stride >= kMaxOffset / 2 ||
-        (c->page_size - 1) * c->token_stride + (c->kv_heads - 1) * c->head_stride + c->head_dim > kMaxOffset)
+    const int64_t page = stride_of(c->page_stride, c->n_pages), head = stride_of(c->head_stride, c->kv_heads);
+    if (!stride_ok(page) || !stride_ok(c->token_stride) || !stride_ok(head) || page >= kMaxOffset ||
+        c->token_stride >= kMaxOffset / 2 || head >= kMaxOffset / 2 ||
+        (c->page_size - 1) * c->token_stride + (c->kv_heads - 1) * head + c->head_dim > kMaxOffset)
         return PROJ_ERR_ARG;
     return PROJ_OK;
 }
@@ -138,9 +139,9 @@ AttnArgs base_args(const blk_cache *c, const blk_batch *b)
     AttnArgs a{};
     a.k = static_cast<const char *>(c->k);
     a.v = static_cast<const char *>(c->v);
-    a.page_stride = (uint32_t)(c->page_stride * 2);
+    a.page_stride = (uint32_t)(stride_of(c->page_stride, c->n_pages) * 2);
     a.token_stride = (int)(c->token_stride * 2);
-    a.head_stride = (int)(c->head_stride * 2);
+    a.head_stride = (int)(stride_of(c->head_stride, c->kv_heads) * 2);
     a.n_pages = c->n_pages;
     a.page_shift = __builtin_ctz((unsigned)c->page_size);
     a.page_mask = c->page_size - 1;
@@ -199,6 +200,8 @@ int blk_kv_append(const blk_cache *cache, const blk_batch *batch, const void *k,
         rc = check_batch(batch);
     if (rc)
         return rc;
+    in_stride = stride_of(in_stride, batch->tokens);
+    in_head_stride = stride_of(in_head_stride, cache->kv_heads);
     if (!stride_ok(in_stride) || !stride_ok(in_head_stride))
         return PROJ_ERR_ARG;
     if (!batch->seqs || !batch->tokens)
@@ -278,8 +281,10 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
     if (args->heads < 1 || args->heads % cache->kv_heads || args->max_q < 1 || args->window < 0 ||
         !(args->scale > 0.f) || !isfinite(args->scale))
         return PROJ_ERR_ARG;
-    for (int64_t s : {args->q_stride, args->q_head_stride, args->gate_stride, args->gate_head_stride, args->out_stride,
-                      args->out_head_stride})
+    auto token_stride = [&](int64_t s) { return stride_of(s, batch->tokens); };
+    auto head_stride = [&](int64_t s) { return stride_of(s, args->heads); };
+    for (int64_t s : {token_stride(args->q_stride), token_stride(args->gate_stride), token_stride(args->out_stride),
+                      head_stride(args->q_head_stride), head_stride(args->gate_head_stride), head_stride(args->out_head_stride)})
         if (!stride_ok(s))
             return PROJ_ERR_ARG;
     if (!batch->seqs || !batch->tokens)
@@ -301,12 +306,12 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
     a.gate = static_cast<const char *>(args->gate);
     a.out = static_cast<char *>(args->out);
     a.lse = args->lse;
-    a.q_stride = args->q_stride * 2;
-    a.q_head = args->q_head_stride * 2;
-    a.gate_stride = args->gate_stride * 2;
-    a.gate_head = args->gate_head_stride * 2;
-    a.out_stride = args->out_stride * 2;
-    a.out_head = args->out_head_stride * 2;
+    a.q_stride = token_stride(args->q_stride) * 2;
+    a.q_head = head_stride(args->q_head_stride) * 2;
+    a.gate_stride = token_stride(args->gate_stride) * 2;
+    a.gate_head = head_stride(args->gate_head_stride) * 2;
+    a.out_stride = token_stride(args->out_stride) * 2;
+    a.out_head = head_stride(args->out_head_stride) * 2;
     a.heads = args->heads;
     a.group = args->heads / cache->kv_heads;
     a.by_group = Divisor::of(a.group);

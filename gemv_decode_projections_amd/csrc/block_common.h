@@ -121,6 +121,10 @@ constexpr int kDeviceScope = 16;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The stride of a dimension, nothing where it has one entry: views carry any
+// number there.
+inline int64_t stride_of(int64_t stride, int64_t count) { return count == 1 ? 0 : stride; }
+
 inline bool aligned_to(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 }  // namespace gdp

@@ -229,7 +229,7 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
         int64_t ks, kh, vs, vh;
         heads_of(k, "k", c, k.size(0), c.kv_heads, dev, ks, kh);
         heads_of(v, "v", c, k.size(0), c.kv_heads, dev, vs, vh);
-        need(ks == vs && (kh == vh || c.kv_heads == 1), "k and v have different strides");
+        need((ks == vs || k.size(0) == 1) && (kh == vh || c.kv_heads == 1), "k and v have different strides");
         const blk_batch b = batch_of(a[3], a[4], a[5], k.size(0), dev);
         if (!is_current(dev))
             return (int)PROJ_ERR_DEVICE;

@@ -211,7 +211,8 @@ extern "C" int blk_norm_run(const blk_norm_args *n, int m, void *stream)
     if (m < 0 || n->width < 1 || n->width > kNormMaxWidth || (n->dtype != BLK_BF16 && n->dtype != BLK_F16) ||
         (n->residual_dtype != n->dtype && n->residual_dtype != BLK_F32))
         return PROJ_ERR_ARG;
-    const int64_t strides[] = {n->x_stride, n->residual_stride, n->gate_stride, n->residual_out_stride, n->out_stride};
+    const int64_t strides[] = {stride_of(n->x_stride, m), stride_of(n->residual_stride, m), stride_of(n->gate_stride, m),
+                               stride_of(n->residual_out_stride, m), stride_of(n->out_stride, m)};
     for (int64_t s : strides)
         if (s < 0 || s >= ((int64_t)1 << 40))
             return PROJ_ERR_ARG;
@@ -242,11 +243,11 @@ extern "C" int blk_norm_run(const blk_norm_args *n, int m, void *stream)
     a.w_pre = static_cast<const char *>(n->weight_pre);
     a.y = static_cast<char *>(n->residual_out);
     a.out = static_cast<char *>(n->out);
-    a.x_stride = n->x_stride * 2;
-    a.residual_stride = n->residual_stride * rb;
-    a.gate_stride = n->gate_stride * 2;
-    a.y_stride = n->residual_out_stride * rb;
-    a.out_stride = n->out_stride * 2;
+    a.x_stride = strides[0] * 2;
+    a.residual_stride = strides[1] * rb;
+    a.gate_stride = strides[2] * 2;
+    a.y_stride = strides[3] * rb;
+    a.out_stride = strides[4] * 2;
     a.width = n->width;
     a.alpha = n->alpha;
     a.eps = n->eps;

@@ -12,8 +12,9 @@
  * checked before the launch (PROJ_ERR_NULL, PROJ_ERR_ALIGN, PROJ_ERR_ARG);
  * lengths, page tables and offsets live on the device and are bounded by the
  * kernels themselves, so no value in them makes a kernel leave its buffers.
- * The library keeps no state between calls: what a call needs beyond its
- * tensors is a buffer of the caller.
+ * Strides are in elements; the stride of a dimension with one entry is not
+ * looked at. The library keeps no state between calls: what a call needs
+ * beyond its tensors is a buffer of the caller.
  */
 #ifndef BLOCK_H
 #define BLOCK_H

@@ -22,3 +22,24 @@ def some_cache(block):  # noqa: F811
 @pytest.mark.parametrize("stride,want", [(0, OK), (1, ARG), (3, ARG), (4, OK), (9, OK), (-1, ARG), (-4, ARG)])
 def test_table_rows_are_one_or_do_not_overlap(block, lib, stride, want):  # noqa: F811
     assert append(lib, some_cache(block), Batch(P, P, P, stride, 4, 2, 0)) == want
+
+
+def test_the_stride_of_a_single_entry_is_not_looked_at(block, lib):  # noqa: F811
+    # (no GPU: a call that passes its checks goes on to the null pointers)
+    from tests.test_block import NULL, Attn, Norm
+
+    vp, ref_ = ctypes.c_void_p, ctypes.byref
+    one = changed(some_cache(block), n_pages=1, kv_heads=1, page_stride=-3, head_stride=5)
+    batch = Batch(P, P, P, 4, 4, 2, 1)
+    for c, want in [(one, NULL), (changed(one, n_pages=2), ARG), (changed(one, kv_heads=2), ARG)]:
+        assert lib.blk_kv_append(ref_(c), ref_(batch), None, None, ctypes.c_int64(3), ctypes.c_int64(5), vp(0)) == want
+    two = changed(batch, tokens=2)
+    assert lib.blk_kv_append(ref_(one), ref_(two), None, None, ctypes.c_int64(3), ctypes.c_int64(5), vp(0)) == ARG
+    args = Attn(0, 0, 0, 0, 65, 7, 3, -1, 1, 9, 1, 1, 0, 0.125)
+    attn = lambda a, b: lib.blk_attn_run(ref_(one), ref_(b), ref_(a), vp(P), ctypes.c_size_t(1 << 40), vp(0))  # noqa: E731
+    assert attn(args, batch) == NULL and attn(args, two) == ARG and attn(changed(args, heads=2), batch) == ARG
+    w = block._W4(64, 256, 128, 0, 0)
+    run = lambda m, xs, os: lib.blk_w4_run(ref_(w), None, None, ctypes.c_int64(xs), m, None, ctypes.c_int64(os), None)  # noqa: E731
+    assert run(1, 13, -1) == NULL and run(2, 13, 64) == ARG and run(2, 256, -1) == ARG
+    n = Norm(0, 0, 0, 0, 0, 0, 0, -1, 3, -5, -7, 1 << 41, 64, 0, 2, 1.0, 1e-6)
+    assert lib.blk_norm_run(ref_(n), 1, None) == NULL and lib.blk_norm_run(ref_(n), 2, None) == ARG

@@ -113,3 +113,46 @@ def test_another_gpu_than_the_cache_or_the_weight(block):
     with pytest.raises(ValueError, match="stream"):
         block.w4_run(w, x, out, stream=Stream())
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_one_token_and_one_head_of_any_stride(block, max_q):
+    # Single rows cut from tensors whose rows are no multiple of 16 bytes apart: the stride is never used.
+    say("single rows", max_q)
+    cache, gen = filled(block, 8, 16, 1, 64)
+    table, q_start, kv_len, ws = ints([[3, 1, 7]]), ints([0, 1]), ints([40]), block.AttnWorkspace(64)
+
+    def odd(shape, offset):
+        # one entry of the first dimension, whose stride is odd
+        inner = math.prod(shape[1:])
+        store = torch.randn(inner * 2 + 19, generator=gen, device=DEV).to(BF)
+        size = [inner * 2 + 3]
+        for n in shape[1:]:
+            size.append(inner // n if len(size) == 1 else 1)
+        return store[offset:].as_strided(shape, size)
+
+    q, gate = odd((1, 4, 64), 0), odd((1, 4, 64), 8)
+    out, plain = odd((1, 4, 64), 16), torch.empty(1, 4, 64, dtype=BF, device=DEV)
+    block.attn_run(q, cache, table, q_start, kv_len, out, ws, max_q=max_q, gate=gate)
+    block.attn_run(q.contiguous(), cache, table, q_start, kv_len, plain, ws, max_q=max_q, gate=gate.contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(out, plain) and bool(torch.isfinite(plain).all())
+    k, v = odd((1, 1, 64), 0), odd((1, 1, 64), 8).as_strided((1, 1, 64), (5, 3, 1))
+    block.kv_append(k, v, cache, table, q_start, kv_len)
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k[7, 7], k[0]) and torch.equal(cache.v[7, 7], v[0])
+    w = block.w4_prepare(torch.randint(0, 256, (24, 32), device=DEV, dtype=torch.uint8), torch.rand(24, 2, device=DEV).to(BF), group=32)
+    x, o, want = odd((1, 64), 0), odd((1, 24), 3), torch.empty(1, 24, dtype=BF, device=DEV)
+    block.w4_run(w, x, o)
+    block.w4_run(w, x.contiguous(), want)
+    r, res, pre = odd((1, 64), 8), odd((1, 64), 0), torch.rand(64, generator=gen, device=DEV).to(BF)
+    y, z = torch.empty(1, 64, dtype=BF, device=DEV), torch.empty(1, 64, dtype=BF, device=DEV)
+    block.norm_run(x, r, y, weight_pre=pre, residual_out=res)
+    block.norm_run(x.contiguous(), r.contiguous(), z, weight_pre=pre, residual_out=torch.empty_like(z))
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(y, z)
+    one = block.KvCache(cache.k[:1].as_strided((1, 16, 1, 64), (77, 64, 3, 1)), cache.v[:1].as_strided((1, 16, 1, 64), (77, 64, 3, 1)))
+    block.attn_run(q, one, ints([[0]]), q_start, ints([9]), out, ws, max_q=max_q)
+    block.attn_run(q, cache, ints([[0]]), q_start, ints([9]), plain, ws, max_q=max_q)
+    torch.cuda.synchronize()
+    assert torch.equal(out, plain)
