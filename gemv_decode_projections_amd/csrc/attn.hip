@@ -202,7 +202,9 @@ int blk_kv_append(const blk_cache *cache, const blk_batch *batch, const void *k,
         return rc;
     in_stride = stride_of(in_stride, batch->tokens);
     in_head_stride = stride_of(in_head_stride, cache->kv_heads);
-    if (!stride_ok(in_stride) || !stride_ok(in_head_stride))
+    if (!stride_ok(in_stride) || !stride_ok(in_head_stride) ||
+        !rows_apart<3>(cache->head_dim, {cache->page_stride, cache->token_stride, cache->head_stride},
+                       {cache->n_pages, cache->page_size, cache->kv_heads}))
         return PROJ_ERR_ARG;
     if (!batch->seqs || !batch->tokens)
         return PROJ_OK;
@@ -287,6 +289,8 @@ int blk_attn_run(const blk_cache *cache, const blk_batch *batch, const blk_attn_
                       head_stride(args->q_head_stride), head_stride(args->gate_head_stride), head_stride(args->out_head_stride)})
         if (!stride_ok(s))
             return PROJ_ERR_ARG;
+    if (!rows_apart<2>(cache->head_dim, {args->out_stride, args->out_head_stride}, {batch->tokens, args->heads}))
+        return PROJ_ERR_ARG;
     if (!batch->seqs || !batch->tokens)
         return PROJ_OK;
     if (!args->q || !args->out || !ws)

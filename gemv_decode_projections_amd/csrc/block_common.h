@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <array>
+
 #include "../../include/block.h"
 #include "../../include/proj.h"
 #include "common.h"
@@ -124,6 +126,28 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // The stride of a dimension, nothing where it has one entry: views carry any
 // number there.
 inline int64_t stride_of(int64_t stride, int64_t count) { return count == 1 ? 0 : stride; }
+
+// Whether rows of `width` elements, counts[i] of them strides[i] apart, lie
+// apart from one another: every dimension steps over all that the closer ones span.
+template <int N>
+bool rows_apart(int64_t width, std::array<int64_t, N> strides, std::array<int64_t, N> counts)
+{
+    int64_t span = width;
+    bool done[N] = {};
+    for (int k = 0; k < N; ++k) {
+        int next = -1;
+        for (int i = 0; i < N; ++i)
+            if (!done[i] && (next < 0 || strides[i] < strides[next]))
+                next = i;
+        done[next] = true;
+        if (counts[next] <= 1)
+            continue;
+        if (strides[next] < span)
+            return false;
+        span += strides[next] * (counts[next] - 1);
+    }
+    return true;
+}
 
 inline bool aligned_to(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 

@@ -216,6 +216,9 @@ extern "C" int blk_norm_run(const blk_norm_args *n, int m, void *stream)
     for (int64_t s : strides)
         if (s < 0 || s >= ((int64_t)1 << 40))
             return PROJ_ERR_ARG;
+    if (!rows_apart<1>(n->width, {n->out_stride}, {m}) ||
+        (n->residual_out && !rows_apart<1>(n->width, {n->residual_out_stride}, {m})))
+        return PROJ_ERR_ARG;
     if (m == 0)
         return PROJ_OK;
     if (!n->residual || !n->weight_pre || !n->out || (n->x && !n->residual_out) ||

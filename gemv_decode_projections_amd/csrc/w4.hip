@@ -384,7 +384,7 @@ int blk_w4_run(const blk_w4 *w, const void *packed, const void *x, int64_t x_str
     x_stride = stride_of(x_stride, m);
     out_stride = stride_of(out_stride, m);
     if (!layout(w, l) || m < 0 || m > (1 << 20) || x_stride < 0 || x_stride % 8 || out_stride < 0 ||
-        x_stride >= ((int64_t)1 << 40) || out_stride >= ((int64_t)1 << 40))
+        x_stride >= ((int64_t)1 << 40) || out_stride >= ((int64_t)1 << 40) || !rows_apart<1>(w->n, {out_stride}, {m}))
         return PROJ_ERR_ARG;
     if (m == 0)
         return PROJ_OK;

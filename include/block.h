@@ -13,7 +13,8 @@
  * lengths, page tables and offsets live on the device and are bounded by the
  * kernels themselves, so no value in them makes a kernel leave its buffers.
  * Strides are in elements; the stride of a dimension with one entry is not
- * looked at. The library keeps no state between calls: what a call needs
+ * looked at. Rows that a call writes must not overlap (PROJ_ERR_ARG); those
+ * that it only reads may. The library keeps no state between calls: what a call needs
  * beyond its tensors is a buffer of the caller.
  */
 #ifndef BLOCK_H

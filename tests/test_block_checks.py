@@ -43,3 +43,37 @@ def test_the_stride_of_a_single_entry_is_not_looked_at(block, lib):  # noqa: F81
     assert run(1, 13, -1) == NULL and run(2, 13, 64) == ARG and run(2, 256, -1) == ARG
     n = Norm(0, 0, 0, 0, 0, 0, 0, -1, 3, -5, -7, 1 << 41, 64, 0, 2, 1.0, 1e-6)
     assert lib.blk_norm_run(ref_(n), 1, None) == NULL and lib.blk_norm_run(ref_(n), 2, None) == ARG
+
+
+def test_outputs_that_overlap_themselves_are_refused(block, lib):  # noqa: F811
+    # (no GPU: a call that passes its checks goes on to the null pointers)
+    from tests.test_block import NULL, Attn, Norm
+
+    vp, ref_ = ctypes.c_void_p, ctypes.byref
+    cache = some_cache(block)
+    batch = Batch(P, P, P, 4, 4, 2, 3)
+    args = Attn(0, 0, 0, 0, 0, 0, 0, 0, 256, 64, 4, 1, 0, 0.125)
+    attn = lambda **kw: lib.blk_attn_run(ref_(cache), ref_(batch), ref_(changed(args, **kw)), vp(P),  # noqa: E731
+                                         ctypes.c_size_t(1 << 40), vp(0))
+    assert attn() == NULL
+    for kw in (dict(out_stride=64, out_head_stride=192), dict(out_stride=1000), dict(out_head_stride=80, out_stride=304)):
+        assert attn(**kw) == NULL, kw                       # apart, in either order
+    for kw in (dict(out_stride=0), dict(out_head_stride=0), dict(out_stride=248), dict(out_head_stride=56),
+               dict(out_stride=64), dict(out_stride=64, out_head_stride=184)):
+        assert attn(**kw) == ARG, kw
+    # keys and values: read through any strides, written only where every place is one
+    none = lambda **kw: lib.blk_kv_append(ref_(changed(cache, **kw)), ref_(batch), None, None, ctypes.c_int64(128),  # noqa: E731
+                                          ctypes.c_int64(64), vp(0))
+    assert none() == NULL and none(token_stride=64, head_stride=1024) == NULL and none(page_stride=4096) == NULL
+    for kw in (dict(page_stride=0), dict(head_stride=0), dict(token_stride=64), dict(page_stride=2040)):
+        assert none(**kw) == ARG, kw
+    shared = Attn(0, 0, 0, 0, 0, 0, 0, 0, 256, 64, 4, 1, 0, 0.125)
+    assert lib.blk_attn_run(ref_(changed(cache, head_stride=0)), ref_(batch), ref_(shared), vp(P), ctypes.c_size_t(1 << 40),
+                            vp(0)) == NULL
+    w = block._W4(64, 256, 128, 0, 0)
+    run = lambda m, os: lib.blk_w4_run(ref_(w), None, None, ctypes.c_int64(0), m, None, ctypes.c_int64(os), None)  # noqa: E731
+    assert run(2, 64) == NULL and run(2, 63) == ARG and run(2, 0) == ARG and run(1, 0) == NULL
+    n = Norm(P, P, 0, 0, P, P, 0, 0, 0, 0, 64, 64, 64, 0, 2, 1.0, 1e-6)
+    norm = lambda m, **kw: lib.blk_norm_run(ref_(changed(n, **kw)), m, None)  # noqa: E731
+    assert norm(2) == NULL and norm(2, os=63) == ARG and norm(2, ys=0) == ARG and norm(1, os=0, ys=0) == NULL
+    assert norm(2, x=0, residual_out=0, ys=0) == NULL
