@@ -14,6 +14,7 @@ library itself refuses raises ProjError (PROJ_ERR_DEVICE: the tensors are on
 one GPU, and another is current).
 """
 
+import array
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -106,6 +107,20 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+def _int32(what, n):
+    """n as the library takes it (a C conversion would drop the upper bits)."""
+    _need(hasattr(n, "__index__") and -2 ** 31 <= n < 2 ** 31, "%s must be an integer of 32 bits, not %r" % (what, n))
+    return int(n)
+
+
+def _page_list(pages):
+    try:
+        a = array.array("i", pages)
+    except (OverflowError, TypeError) as e:
+        raise ValueError("page numbers must be integers of 32 bits: %s" % e) from None
+    return (ctypes.c_int32 * len(a)).from_buffer(a) if len(a) else (ctypes.c_int32 * 0)()
+
+
 class KvCache:
     """A paged cache over the tensors k and v, pages x page_size x kv_heads x head_dim
     (BF16 or FP16; any strides with the last one 1, so permuted views of head-major
@@ -162,7 +177,7 @@ class PagePool:
     sequences use too is first replaced by writable(), which says what to copy."""
 
     def __init__(self, n_pages):
-        self.n_pages = int(n_pages)
+        self.n_pages = _int32("n_pages", int(n_pages))
         handle = _vp()
         _fail(_lib().blk_pool_create(self.n_pages, ctypes.byref(handle)), "PagePool(%d)" % self.n_pages)
         self._handle = handle
@@ -177,24 +192,24 @@ class PagePool:
         return _lib().blk_pool_free_pages(self._handle)
 
     def users(self, page):
-        n = _lib().blk_pool_users(self._handle, page)
+        n = _lib().blk_pool_users(self._handle, _int32("page", page))
         _fail(min(n, 0), "users(%d)" % page)
         return n
 
     def alloc(self, n):
         """The n lowest free pages; ProjError (PROJ_ERR_PAGES), and none taken, if there are fewer."""
-        pages = (ctypes.c_int32 * max(n, 0))()
+        pages = (ctypes.c_int32 * max(_int32("n", n), 0))()
         _fail(_lib().blk_pool_alloc(self._handle, n, pages), "alloc(%d)" % n)
         return list(pages)
 
     def fork(self, pages):
         """Another sequence's list of the same pages: each gets one more user."""
-        _fail(_lib().blk_pool_share(self._handle, (ctypes.c_int32 * len(pages))(*pages), len(pages)), "fork")
+        _fail(_lib().blk_pool_share(self._handle, _page_list(pages), len(pages)), "fork")
         return list(pages)
 
     def free(self, pages):
         """Takes one user from each page; pages without users are free again."""
-        _fail(_lib().blk_pool_release(self._handle, (ctypes.c_int32 * len(pages))(*pages), len(pages)), "free")
+        _fail(_lib().blk_pool_release(self._handle, _page_list(pages), len(pages)), "free")
 
     def writable(self, pages, index):
         """Makes pages[index] this sequence's own before a write: (old, new) to be copied if others
@@ -212,7 +227,7 @@ class PagePool:
     def compact(self, max_moves=None):
         """Moves of pages down into free ones: (src, dst), as kv_copy_pages takes them. Replace src[i]
         by dst[i] in every page list (remap) and table."""
-        n = self.n_pages if max_moves is None else max_moves
+        n = self.n_pages if max_moves is None else _int32("max_moves", max_moves)
         src, dst = (ctypes.c_int32 * max(n, 0))(), (ctypes.c_int32 * max(n, 0))()
         moves = _lib().blk_pool_compact(self._handle, n, src, dst)
         _fail(min(moves, 0), "compact(%s)" % max_moves)

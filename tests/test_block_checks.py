@@ -77,3 +77,21 @@ def test_outputs_that_overlap_themselves_are_refused(block, lib):  # noqa: F811
     norm = lambda m, **kw: lib.blk_norm_run(ref_(changed(n, **kw)), m, None)  # noqa: E731
     assert norm(2) == NULL and norm(2, os=63) == ARG and norm(2, ys=0) == ARG and norm(1, os=0, ys=0) == NULL
     assert norm(2, x=0, residual_out=0, ys=0) == NULL
+
+
+def test_page_numbers_past_32_bits_are_refused(block):  # noqa: F811
+    # 2^32 + 1 is not page 1.
+    pool = block.PagePool(6)
+    pages = pool.alloc(3)
+    for bad in ([2 ** 32 + 1], [0, 2 ** 31], [-2 ** 31 - 1], [1.0], ["1"], [None]):
+        with pytest.raises(ValueError):
+            pool.free(bad)
+        with pytest.raises(ValueError):
+            pool.fork(bad)
+    for call in (lambda: pool.users(2 ** 32 + 1), lambda: pool.alloc(2 ** 32 + 1), lambda: pool.compact(2 ** 32 + 1),
+                 lambda: pool.writable([2 ** 32 + 1], 0), lambda: block.PagePool(2 ** 32 + 1), lambda: pool.alloc(1.5)):
+        with pytest.raises(ValueError):
+            call()
+    assert [pool.users(p) for p in range(6)] == [1, 1, 1, 0, 0, 0] and pool.free_pages == 3
+    pool.free(pages)
+    assert pool.free_pages == 6 and pool.fork([]) == [] and pool.free(()) is None
