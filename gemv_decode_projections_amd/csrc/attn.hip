@@ -163,6 +163,39 @@ int launch(const void *fn, dim3 grid, dim3 block, void *arg, void *stream)
     return e == hipSuccess ? PROJ_OK : hip_fail(e);
 }
 
+// Up to n page numbers, in a table of their own number, not the cache's: a fork
+// of one page costs the same in a cache of any size.
+class PageSet {
+    std::vector<uint32_t> slots;       // page + 1, or 0
+    int shift;
+
+    size_t find(uint32_t key) const    // the key's slot, or the free one for it
+    {
+        size_t i = (key * 2654435769u) >> shift;
+        while (slots[i] && slots[i] != key)
+            i = (i + 1) & (slots.size() - 1);
+        return i;
+    }
+
+public:
+    explicit PageSet(int n)
+    {
+        int bits = 2;
+        while (((int64_t)1 << bits) < 2 * (int64_t)n)
+            ++bits;
+        slots.assign((size_t)1 << bits, 0);
+        shift = 32 - bits;
+    }
+    bool has(int32_t page) const { return slots[find((uint32_t)page + 1)] != 0; }
+    bool add(int32_t page)             // false if it was there
+    {
+        uint32_t &slot = slots[find((uint32_t)page + 1)];
+        const bool fresh = !slot;
+        slot = (uint32_t)page + 1;
+        return fresh;
+    }
+};
+
 template <class I>
 int copy_pages(const blk_cache *cache, const int32_t *src, const int32_t *dst, int n, int64_t elems, void *stream)
 {
@@ -251,15 +284,12 @@ int blk_kv_copy_pages(const blk_cache *cache, const int32_t *src, const int32_t 
         return PROJ_ERR_ARG;
     try {
         // A page is written once at most, and none both read and written.
-        std::vector<uint8_t> use(cache->n_pages, 0);
-        for (int i = 0; i < n; ++i) {
-            if (src[i] < 0 || src[i] >= cache->n_pages || dst[i] < 0 || dst[i] >= cache->n_pages || (use[dst[i]] & 2))
-                return PROJ_ERR_ARG;
-            use[src[i]] |= 1;
-            use[dst[i]] |= 2;
-        }
+        PageSet written(n);
         for (int i = 0; i < n; ++i)
-            if (use[dst[i]] & 1)
+            if (src[i] < 0 || src[i] >= cache->n_pages || dst[i] < 0 || dst[i] >= cache->n_pages || !written.add(dst[i]))
+                return PROJ_ERR_ARG;
+        for (int i = 0; i < n; ++i)
+            if (written.has(src[i]))
                 return PROJ_ERR_ARG;
     } catch (const std::bad_alloc &) {
         return PROJ_ERR_HIP;

@@ -95,3 +95,49 @@ def test_page_numbers_past_32_bits_are_refused(block):  # noqa: F811
     assert [pool.users(p) for p in range(6)] == [1, 1, 1, 0, 0, 0] and pool.free_pages == 3
     pool.free(pages)
     assert pool.free_pages == 6 and pool.fork([]) == [] and pool.free(()) is None
+
+
+def test_a_fork_in_a_large_cache_costs_what_it_copies(block):  # noqa: F811
+    # The check of the pairs must not take memory by the cache's size: two pairs, 2^31 - 1 pages. In a
+    # process of its own, whose peak memory says so.
+    import os
+    import subprocess
+    import sys
+
+    program = """
+import ctypes, resource
+from gemv_decode_projections_amd import block
+lib = block._lib()
+cache = block._Cache(4096, 4096, 16 * 64, 64, 64, 2 ** 31 - 1, 16, 1, 64, 0)
+pages = ctypes.c_int32 * 2
+peak = lambda: resource.getrusage(resource.RUSAGE_SELF).ru_maxrss
+before = peak()
+for s, d in [((0, 2 ** 31 - 3), (5, 5)), ((0, 2 ** 31 - 2), (2 ** 31 - 2, 9)), ((0, 1), (2 ** 31 - 1, 9))]:
+    assert lib.blk_kv_copy_pages(ctypes.byref(cache), pages(*s), pages(*d), 2, None) == -10
+print(peak() - before)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
+    assert int(r.stdout) < 64 * 1024, r.stdout        # KB
+
+
+def test_page_pairs_against_a_plain_check(block, lib):  # noqa: F811
+    # Pairs that must be refused are (no GPU: accepted ones fail in the launch, which is another status).
+    import random
+
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("would launch copies at made-up addresses")
+    rng = random.Random(4)
+    for pages in (3, 40, 70000, 2 ** 31 - 1):
+        cache = block._Cache(P, P, 16 * 64, 64, 64, pages, 16, 1, 64, 0)
+        for _ in range(300):
+            n = rng.randint(1, 40)
+            near = rng.choice([pages, min(pages, 2 * n + 2)])
+            src, dst = ([rng.randrange(near) for _ in range(n)] for _ in range(2))
+            bad = len(set(dst)) < n or set(src) & set(dst)
+            a = (ctypes.c_int32 * n)
+            rc = lib.blk_kv_copy_pages(ctypes.byref(cache), a(*src), a(*dst), n, ctypes.c_void_p(0))
+            assert (rc == ARG) == bool(bad), (pages, src, dst, rc)
