@@ -156,3 +156,59 @@ def test_one_token_and_one_head_of_any_stride(block, max_q):
     block.attn_run(q, cache, ints([[0]]), q_start, ints([9]), plain, ws, max_q=max_q)
     torch.cuda.synchronize()
     assert torch.equal(out, plain)
+
+
+FIRST_CALLS = """
+import torch
+from gemv_decode_projections_amd import block
+
+BF, DEV = torch.bfloat16, "cuda"
+g = torch.Generator(DEV).manual_seed(0)
+rand = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF)
+ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+ws, cache, parts = block.AttnWorkspace(128), block.KvCache(rand(240, 16, 1, 128), rand(240, 16, 1, 128)), []
+for i, new in enumerate((1, 3, 8, 40)):         # every kind of kernel, with parts to be joined; each its own pages
+    parts.append((rand(new, 8, 128), rand(new, 1, 128), ints([0, new]), ints([900]), torch.zeros(new, 8, 128, dtype=BF, device=DEV),
+                  ints([list(range(57 * i, 57 * i + 57))])))
+w = block.w4_prepare(torch.randint(0, 256, (320, 512), generator=g, device=DEV, dtype=torch.uint8), torch.rand(320, 8, generator=g, device=DEV).to(BF) / 64)
+x, o, r, y = rand(4, 1024), torch.zeros(4, 320, dtype=BF, device=DEV), torch.randn(4, 320, generator=g, device=DEV), rand(4, 320)
+out, pre, ro = torch.zeros_like(y), rand(320), torch.zeros_like(r)
+
+
+def step():
+    for q, k, start, length, dst, table in parts:
+        block.kv_append(k, k, cache, table, start, length)
+        block.attn_run(q, cache, table, start, length, dst, ws, max_q=q.shape[0])
+    block.kv_copy_pages(cache, [1, 2], [238, 239])
+    block.w4_run(w, x, o)
+    block.norm_run(y, r, out, weight_pre=pre, residual_out=ro)
+
+
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    step()
+results = [p[4] for p in parts] + [o, out, ro, cache.k]
+for i in range(3):
+    for t in [x, y] + [p[1] for p in parts]:
+        t.copy_(rand(*t.shape))
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = [t.clone() for t in results]
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) and bool(a.float().abs().sum() > 0) for a, b in zip(replayed, results)), i
+print("replays match")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    # No launch of any of the kernels before the capture.
+    import os
+    import subprocess
+    import sys
+
+    say("first calls captured")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "replays match" in r.stdout, r.stdout + r.stderr
