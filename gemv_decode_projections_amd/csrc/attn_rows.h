@@ -53,6 +53,9 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
     constexpr int HALF = DIM / (16 * VEC);           // 16 * VEC element blocks of a value row
     constexpr int PITCH = DIM + 4;
     constexpr int STEP = 32;
+    // The largest weight is 2^ABOVE, in FP16 the largest power of the type: weights
+    // down to 2^-29 of it are normal numbers.
+    constexpr float ABOVE = T::kId == BLK_F16 ? 15.0f : 0.0f;
     constexpr int PER = DIM / 4;               // threads per row when rows leave
     constexpr int RSTEP = 64 * WAVES / PER;    // rows per pass then
     constexpr int PASSES = (ROWS + RSTEP - 1) / RSTEP;
@@ -245,7 +248,7 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
                     s[nb][t][i] *= a.scale_log2;
                     m = fmaxf(m, s[nb][t][i]);
                 }
-            m = fmaxf(top[nb], max_quads(m));
+            m = fmaxf(top[nb], max_quads(m) - ABOVE);
             if (__any(m > top[nb])) {
                 const float f = exp2_fast(top[nb] - (m == -INFINITY ? 0.f : m));
                 top[nb] = m;
@@ -264,8 +267,8 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
                 sum[nb] += p[e];
             }
             // Probabilities in 16 bits for the matrix instruction: each within
-            // half a unit of the type, errors that average out over a row;
-            // the sum keeps the unrounded ones.
+            // half a unit of the type, errors that average out over a row (the
+            // largest is a power of two); the sum keeps the unrounded ones.
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 pf[nb][e] = T::pack(p[2 * e], p[2 * e + 1]);

@@ -14,8 +14,8 @@
 // transposing LDS read hands each lane four such positions of one element.
 //
 // The rows' maximum is raised only when a score passes it by more than 2^8 (in
-// powers of two): the weights then stay below 2^8, exact in FP32 and in the
-// types' range, and the accumulators are rescaled a few times per row instead
+// powers of two): the weights then stay below 2^8 (FP16: 2^15), exact in FP32
+// and in the types' range, and the accumulators are rescaled a few times per row instead
 // of once per tile.
 //
 // Tiles of K and V fill a ring of LDS by DMA, one tile ahead of the products. A
@@ -76,7 +76,9 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
     constexpr int TILEB = POS * ROWB;                // bytes of one tile of K or V
     constexpr int RPI = 1024 / ROWB;                 // rows per DMA instruction (8, 4 or 2)
     constexpr int NI = POS / RPI / WAVES;       // DMA instructions per wave and tile, of K as of V
-    constexpr float RAISE = 8.0f;
+    // (FP16: the largest weight is 2^7 to 2^15, and those down to 2^-21 of it are
+    // normal numbers of the type)
+    constexpr float RAISE = 8.0f, ABOVE = T::kId == BLK_F16 ? 15.0f - RAISE : 0.0f;
     // The ring of tiles; at the end each wave's 32 rows in FP32, 16-byte pieces
     // permuted so that neither side meets a bank conflict.
     constexpr int OUTB = ROWS * DIM * 4;
@@ -220,8 +222,8 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
         for (int i = 1; i < 16 * HALVES; ++i)
             m = __builtin_elementwise_maximum(m, s[i / 16][i % 16]);
         m = max32(m) * a.scale_log2;
-        if (__any(m > top + RAISE)) {
-            const float raised = fmaxf(m, top);
+        if (__any(m > top + (ABOVE + RAISE))) {
+            const float raised = fmaxf(m - ABOVE, top);
             const float f = exp2_fast(top - (raised == -INFINITY ? 0.f : raised));
             top = raised;
             sum *= f;
