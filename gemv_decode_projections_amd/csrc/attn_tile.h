@@ -158,7 +158,7 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
 #pragma unroll
     for (int d = 0; d < DB; ++d)
         acc[d] = f32x16{};
-    float top = -INFINITY, sum = 0.f;
+    float most = -INFINITY, top = -INFINITY, sum = 0.f;      // the row's largest score, what weights are relative to
 
     // Value fragment of positions k0 + 4 half + {0..3, 8..11}, element 32 d +
     // col, by two transposing reads: of each 16 lanes, lane i points at row
@@ -221,9 +221,12 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
 #pragma unroll
         for (int i = 1; i < 16 * HALVES; ++i)
             m = __builtin_elementwise_maximum(m, s[i / 16][i % 16]);
-        m = max32(m) * a.scale_log2;
-        if (__any(m > top + (ABOVE + RAISE))) {
-            const float raised = fmaxf(m - ABOVE, top);
+        most = fmaxf(most, max32(m));
+        m = most * a.scale_log2;
+        const bool passes = m > top + (ABOVE + RAISE);
+        if (__any(passes)) {
+            // (this row only if it has to: `top` is then as it was when `most` was weighed)
+            const float raised = passes ? m - ABOVE : top;
             const float f = exp2_fast(top - (raised == -INFINITY ? 0.f : raised));
             top = raised;
             sum *= f;
@@ -234,7 +237,8 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
     };
     // Probabilities in 16 bits for the matrix instruction: each within half a
     // unit of the type, errors that average out over a row; the sum keeps the
-    // unrounded ones.
+    // unrounded ones. (The largest's does not average out where it dominates:
+    // see `even`.)
     auto weights = [&](const f32x16 &s, u32x4 (&pf)[2]) {
         const float safe = top == -INFINITY ? 0.f : top;
 #pragma unroll
@@ -370,14 +374,18 @@ __global__ __launch_bounds__(64 * WAVES, DIM < 256 && WAVES > 2 ? 2 : 1) void at
     __syncthreads();
     constexpr int PIECES_O = DIM / 4;                // 16-byte pieces of a row
     char *rows = s_mem + wave * 32 * DIM * 4;
+    sum = sum32(sum);
+    // A row is divided by its weights' sum as they were rounded, as far as the
+    // largest goes: one key alone gives its value. (1: nothing seen, or NaN)
+    const float p0 = exp2_fast(__builtin_fmaf(most, a.scale_log2, -top));
+    const float even = sum > 0.f ? sum / (sum + (T::lo(T::pack(p0, p0)) - p0)) : 1.f;
     auto place = [](int row, int p) { return (row * PIECES_O + (p ^ (row % 16))) * 16; };
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
             *reinterpret_cast<f32x4 *>(rows + place(col, 8 * d + 2 * g + half)) =
-                f32x4{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
-    sum = sum32(sum);
+                f32x4{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]} * even;
     if (u.splits == 1 && half == 0 && r < u.nrows)
         write_lse(a, tok, head, top, sum);
     const Slots<DIM, ROWS, 0> slots(a);

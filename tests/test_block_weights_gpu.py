@@ -59,3 +59,23 @@ def test_a_flat_tail_below_a_sink_keeps_its_bits_in_fp16(block, new, heads, dim)
     ref.assert_within("out", out, want, (2.0 ** -10 + 2.0 ** -18) * want.abs())
     # (as in block_ref: scores and lse of 14.5 in FP32, a sum of 4097 terms)
     ref.assert_within("lse", lse, logs, 2.0 ** -18 + 4097 * 2.0 ** -23 + 2.0 ** -20 * logs.abs())
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("new,heads", [(1, 8), (3, 8), (8, 8), (100, 4)])
+@pytest.mark.parametrize("gap", [3.3, 5.0, 5.4])
+def test_a_dominant_key_in_a_later_tile_keeps_its_weight(block, dtype, new, heads, gap):
+    # One key, and `gap` above it another some tiles later; the rest weigh nothing. The later one's
+    # value comes back as the formula gives it: its weight is not rounded against the sum's, the earlier
+    # one's is, by u of its share e^-gap; an output is rounded by half a step of its type.
+    say("dominant", dtype, new, heads, gap)
+    dim, total = 128, 400
+    scores, values = torch.zeros(total), torch.zeros(total, dim)
+    scores[0], scores[200] = 30.0, torch.tensor(30.0 + gap).to(dtype).float()
+    values[200] = (1 + torch.arange(dim) / dim).to(dtype).float()
+    out, _, want, _ = scored(block, scores, values, new, heads, dim, dtype)
+    u = ref.U[dtype]
+    want = want.contiguous()
+    more = want.abs() * (u * math.exp(-gap) + 2.0 ** -18)
+    half_step = u * 2.0 ** torch.floor(torch.log2(want.abs() + more))
+    ref.assert_within("out", out, want, half_step + more)
