@@ -432,7 +432,8 @@ using AttnKernel = void (*)(AttnArgs);
 AttnKernel attn_rows_kernel(int dtype, int dim, int nb);
 // Tile kernels for tiles of 64 or 128 rows, two threads per row.
 AttnKernel attn_tile_kernel(int dtype, int dim, int rows);
-// Join kernels for tiles of 16, 32, 64 or 128 rows, kJoinThreads threads.
+// Join kernels for tiles of 32, 64 or 128 rows (the row kernel joins its tiles of
+// 16 itself), kJoinThreads threads.
 AttnKernel attn_join_kernel(int dtype, int dim, int rows);
 constexpr int kJoinThreads = 256;
 

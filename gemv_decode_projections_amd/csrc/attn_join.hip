@@ -7,7 +7,6 @@ template <class T, int DIM>
 static AttnKernel pick(int rows)
 {
     switch (rows) {
-    case 16: return attn_join<T, DIM, 16>;
     case 32: return attn_join<T, DIM, 32>;
     case 64: return attn_join<T, DIM, 64>;
     case 128: return attn_join<T, DIM, 128>;
