@@ -14,10 +14,10 @@
 // weight byte). A workgroup owns RB blocks of 16 rows and 16 NT tokens; its
 // waves split K, each unit of 128 k is one 16-byte load per lane and row
 // block, 1 KB contiguous per wave. Measured, BF16: 2304 x 8192, groups of 128,
-// one token: 5.5 us (9.9 MB at 1.8 TB/s: 144 row blocks fill little over half
-// the card, and the time is a launch, one load's latency and the join of the
-// waves); 8192 x 4096, groups of 64, 32 tokens: 9.5 us, bound by the
-// activations that every workgroup reads from L2.
+// one token: 6.4 us (9.9 MB at 1.5 TB/s: 144 row blocks fill little over half
+// the card, and the time is a launch, two loads' latency, the operands and the
+// join of the waves); 8192 x 4096, groups of 64, 32 tokens: 9.8 us, bound by
+// the activations that every workgroup reads from L2.
 #include <limits.h>
 
 #include "block_common.h"
@@ -75,9 +75,9 @@ __device__ __forceinline__ u32x4 weight_operand(uint32_t w, uint32_t z, uint32_t
 // Activations are read along the rows, 256 bytes per 16 lanes, and turned to
 // operands (column l % 16, k 8 (l / 16) + 0..7 of each 32) by way of LDS,
 // 16-byte pieces permuted so that neither side meets a bank conflict: read as
-// operands, every four lanes would touch four rows (2304 x 8192, 16 tokens:
-// 10.2 us, this way 6.5). DIRECT reads them as operands all the same: for one
-// or two tokens the lanes' rows coincide (one token: 5.5 us against 6.1).
+// operands, every four lanes would touch four rows (8192 x 3968, 16 tokens:
+// 10.4 us, this way 8.1). DIRECT reads them as operands all the same: for one
+// or two tokens the lanes' rows coincide (one token: 6.2 us against 7.6).
 template <class T, int G, int RB, int NT, int CH, int WAVES, bool DIRECT>
 __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a)
 {
@@ -280,29 +280,42 @@ struct W4Plan {
     int rb, nt, waves;
 };
 
-// Tiles by token count and row blocks; measured (us) on the shapes in brackets.
+// Rounds that `wgs` workgroups take, one per compute unit at a time.
+int rounds(int64_t wgs) { return (int)((wgs + 255) / 256); }
+
+// Row blocks per workgroup by the rounds that result, times what a round takes
+// relative to the others. (Times in us, BF16, no zeros, k = 8192 if not stated.
+// 4096 rows are one round of one block, 5120 the first two.)
+//   up to 16 tokens   4096 rows: one block 8.1, two 10.8; 5120 rows: 12.6, 10.6;
+//                     12288 rows: 18.9, 16.8: 3 to 4
+//   more, tiles of 32 32 tokens, 4096 rows: one block 11.3, two 13.2, four 20.6;
+//                     5120 rows: 16.7, 13.1, 20.6; 12288 rows: 23.3, 24.2, 22.1;
+//                     64 tokens, 12288 rows: 42.3, 36.7, 40.4; 1000 tokens, 8192
+//                     rows: 414, 357, 298: 17 to 20 to 32
 template <class T, int G>
 W4Plan pick(int m, int blocks, int units)
 {
-    const bool many = blocks >= 512;       // two row blocks per workgroup still fill the chip
     if (m <= 16) {
-        // Short k: one unit per wave and turn.
+        const bool two = 4 * rounds((blocks + 1) / 2) < 3 * rounds(blocks);
+        // Short k: one unit per wave and turn (k = 2048, 8192 rows, 4 tokens: 4.5;
+        // two of 16 waves 6.1).
         if (units < 32)
-            return many ? W4Plan{w4_kernel<T, G, 2, 1, 1, 8, false>, 2, 1, 8}
-                        : W4Plan{w4_kernel<T, G, 1, 1, 1, 8, false>, 1, 1, 8};
+            return two ? W4Plan{w4_kernel<T, G, 2, 1, 1, 8, false>, 2, 1, 8}
+                       : W4Plan{w4_kernel<T, G, 1, 1, 1, 8, false>, 1, 1, 8};
+        // (one token, 4096 rows: 6.9, the next 7.5; 12288 rows: 15.0, two blocks 16.5)
         if (m <= 2)
             return {w4_kernel<T, G, 1, 1, 4, 8, true>, 1, 1, 8};
-        return {w4_kernel<T, G, 1, 1, 2, 16, false>, 1, 1, 16};
+        return two ? W4Plan{w4_kernel<T, G, 2, 1, 1, 8, false>, 2, 1, 8}
+                   : W4Plan{w4_kernel<T, G, 1, 1, 2, 16, false>, 1, 1, 16};
     }
-    // 8192 x 4096, 32 tokens: 9.6 with two row blocks and 16 waves, 12.6 with
-    // one; 2304 x 8192: 11.7 and 10.3.
-    if (m <= 32 && !many)
+    const int64_t tiles = (m + 31) / 32;
+    const int64_t one = 17ll * rounds(blocks * tiles), two = 20ll * rounds((blocks + 1) / 2 * tiles),
+                  four = 32ll * rounds((blocks + 3) / 4 * tiles);
+    if (one <= two && one <= four)
         return {w4_kernel<T, G, 1, 2, 2, 8, false>, 1, 2, 8};
-    // 64 tokens in two tiles, 8192 x 4096: 15.2 with four row blocks, 17.6 with
-    // two; 2304 x 8192: 18.1 and 12.3.
-    if (m > 32 && many)
-        return {w4_kernel<T, G, 4, 2, 2, 8, false>, 4, 2, 8};
-    return {w4_kernel<T, G, 2, 2, 1, 16, false>, 2, 2, 16};
+    if (two <= four)
+        return {w4_kernel<T, G, 2, 2, 1, 16, false>, 2, 2, 16};
+    return {w4_kernel<T, G, 4, 2, 2, 8, false>, 4, 2, 8};
 }
 
 template <class T>

@@ -105,3 +105,18 @@ def test_a_large_activation_on_zero_weights_leaves_no_trace(block, dtype, big, m
         q[:, c // 2] = pair & 0x0f | zc << 4 if c % 2 else pair & 0xf0 | zc
     out = run(block, q, s, z, group, x)
     ref.assert_within("w4", out, *direct(q, s, z, group, x))
+
+
+@pytest.mark.parametrize("m", [1, 5, 16, 17, 33, 64, 65, 100, 260])
+@pytest.mark.parametrize("n,k", [(1000, 256), (4100, 64), (4112, 4096), (8200, 128), (5000, 4128), (12300, 96)])
+def test_every_tile_that_the_rule_picks(block, m, n, k):
+    # Row blocks on both sides of one, two and three rounds of workgroups, and token counts with and
+    # without a part of a tile; the sum over a few rows is enough to see a block or tile misplaced.
+    say("w4 plans", m, n, k)
+    q, s, z, g = weights(n, k, 32, True, BF, 5)
+    x = torch.randn(m, k, generator=g).to(BF)
+    out = run(block, q, s, z, 32, x)
+    rows = sorted({0, 1, 15, 16, 17, 33, 63, 64, n // 2, n - 17, n - 16, n - 15, n - 2, n - 1})
+    r, b = direct(q[rows], s[rows], z[rows], 32, x)
+    ref.assert_within("w4", out[:, rows], r, b)
+    assert bool(torch.isfinite(out).all())
