@@ -53,6 +53,7 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
     constexpr int HALF = DIM / (16 * VEC);           // 16 * VEC element blocks of a value row
     constexpr int PITCH = DIM + 4;
     constexpr int STEP = 32;
+    constexpr bool TWO_PARTS = NB == 1;              // of the probabilities
     // The largest weight is 2^ABOVE, in FP16 the largest power of the type: weights
     // down to 2^-29 of it are normal numbers.
     constexpr float ABOVE = T::kId == BLK_F16 ? 15.0f : 0.0f;
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
                         for (int e = 0; e < VEC / 2; ++e)
                             vr[h][p][e] = finite_only<T>(vr[h][p][e]);
         }
-        u32x4 pf[NB];
+        u32x4 pf[NB], rest[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             float m = -INFINITY;
@@ -268,10 +269,15 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
             }
             // Probabilities in 16 bits for the matrix instruction: each within
             // half a unit of the type, errors that average out over a row (the
-            // largest is a power of two); the sum keeps the unrounded ones.
+            // largest is a power of two); the sum keeps the unrounded ones. Of
+            // 16 rows what rounding left is multiplied as well, in the time
+            // that the loads take anyway (of 32 rows of 256 it takes 12 %).
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e) {
                 pf[nb][e] = T::pack(p[2 * e], p[2 * e + 1]);
+                if constexpr (TWO_PARTS)
+                    rest[nb][e] = T::pack(p[2 * e] - T::lo(pf[nb][e]), p[2 * e + 1] - T::hi(pf[nb][e]));
+            }
         }
 #pragma unroll
         for (int h = 0; h < HALF; ++h) {
@@ -280,8 +286,11 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
 #pragma unroll
             for (int j = 0; j < VEC; ++j)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+                for (int nb = 0; nb < NB; ++nb) {
+                    if constexpr (TWO_PARTS)
+                        acc[nb][h][j] = T::mfma16(vt[j], rest[nb], acc[nb][h][j]);
                     acc[nb][h][j] = T::mfma16(vt[j], pf[nb], acc[nb][h][j]);
+                }
         }
         if (poisoned)
             for (int pos = 0; pos < STEP; ++pos) {

@@ -79,3 +79,22 @@ def test_a_dominant_key_in_a_later_tile_keeps_its_weight(block, dtype, new, head
     more = want.abs() * (u * math.exp(-gap) + 2.0 ** -18)
     half_step = u * 2.0 ** torch.floor(torch.log2(want.abs() + more))
     ref.assert_within("out", out, want, half_step + more)
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 4, 2), (128, 8, 1), (256, 5, 1)])
+@pytest.mark.parametrize("cached", [0, 31, 700, 5000])
+def test_single_tokens_weigh_with_more_than_their_types_bits(block, dtype, dim, heads, kv_heads, cached):
+    # The bound of block_ref but for the weights' rounding: in two parts of 16 bits u^2 is left of it.
+    say("two parts", dtype, dim, cached)
+    from tests.test_block_gpu import make_batch, run_attn
+
+    cache, table, q_start, kv_len, gen = make_batch(block, [1, 1], [cached, cached // 2], 16, kv_heads, dim, dtype, 4)
+    q = torch.randn(2, heads, dim, generator=gen).to(dtype).to(DEV)
+    out, lse = run_attn(block, cache, table, q_start, kv_len, q, max_q=1)
+    args = (table, q_start, kv_len, dim ** -0.5)
+    want, logs, bound, log_bound = ref.attention(q, cache.k, cache.v, *args)
+    size = ref.attention(q, cache.k, cache.v.abs(), *args)[0]
+    u = ref.U[dtype]
+    ref.assert_within("out", out, want, bound - (1 + u) * (u - u * u) * size)
+    ref.assert_within("lse", lse, logs, log_bound)
