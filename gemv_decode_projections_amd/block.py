@@ -155,6 +155,7 @@ class KvCache:
 def kv_append(k, v, cache, table, q_start, kv_len, stream=None):
     """Write the new tokens' keys and values (tokens x kv_heads x head_dim) into their pages.
 
+    k and v may be views of a projection's output, with the same strides.
     table (seqs x pages), q_start (seqs + 1) and kv_len (seqs, the new tokens included) are int32 on
     the device; a token at a negative position or on an unmapped page is not written."""
     rc = _ext().kv_append(cache._addr, k, v, table, q_start, kv_len, _raw_stream(stream, cache._index))
@@ -261,7 +262,7 @@ def attn_run(q, cache, table, q_start, kv_len, out, ws, *, max_q=None, scale=Non
     times sigmoid(gate) if given.
 
     A token sees the positions up to its own (the last `window` of them if window > 0); heads share
-    key heads in groups. lse (float32, tokens x heads) receives the log of the sums of exponentials.
+    key heads in groups. Tokens of no sequence (from q_start[-1] on) are left as they are. lse (float32, tokens x heads) receives the log of the sums of exponentials.
     max_q is the largest number of new tokens of a sequence (default: all of them): it picks the
     kernel, not the result."""
     if ws.head_dim < cache.head_dim or ws.index != cache._index:

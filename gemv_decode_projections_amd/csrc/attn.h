@@ -132,12 +132,16 @@ __device__ __forceinline__ void seq_bounds(const AttnArgs &a, int b, int &tok0, 
 //     x 8 heads: 640 units in 512 places took 139 us, 512 in 128);
 //   - row kernels, with much work per unit or more tiles than half the places:
 //     several rounds of smaller parts even out better (2048 units: 121 us);
-//   - row kernels: short parts are not worth a join: up to 512 positions per
-//     part as long as a tile has no more than 16 parts and half the places are
-//     taken (one token over 131072 positions: 256 parts 20.5 us, 512 parts 24);
+//   - row kernels: short parts are not worth a join: up to 512 positions (640,
+//     rounded up) per part as long as a tile has no more than 16 parts and half
+//     the places are taken (one token over 131072 positions: 256 parts 20.5 us,
+//     512 parts 24);
 //   - tile kernels, with more tiles than half the places: the join of 128 rows
 //     costs more than an uneven round, so C is twice that (416 tiles: 288 us,
 //     cut for 512 places 446; 256 tiles cut in two: 177 us, whole 203).
+// (Each pair of times is of the kernels as they were when the choice was made:
+// the difference counts.) A tile's range is its sequence's, not what the tile
+// sees: of a prompt with nothing cached the later tiles are the longer ones.
 // (All of it inlined: called as functions, a unit's fields come back through
 // memory and are no longer scalars.)
 template <int ROWS>
@@ -275,10 +279,10 @@ struct Partition {
 // The workgroup's unit; false for workgroups past the last one. Workgroups are
 // dealt to the 8 XCDs round-robin; the units are given to the XCDs in
 // contiguous eighths. The heads of a key come first, as they lie next to each
-// other in a page (with the heads apart in time 32 sequences x 8 heads took
-// 145 us instead of 131), then the row tiles, which share their keys in an L2
-// (chunks of 1000 and 630 tokens: 282 us, though the L2s fetch 545 MB; tiles
-// before heads 289 and 119 MB).
+// other in a page (32 sequences x 8 heads, when it was chosen: 131 us, with the
+// heads apart in time 145), then the row tiles, which share their keys in an L2
+// (chunks of 1000 and 630 tokens in pages of 16: 282 us, though the L2s fetch
+// 540 MB; tiles before heads 289 and 119 MB; not measured on other contexts).
 template <int ROWS>
 __device__ __forceinline__ bool find_unit(const AttnArgs &a, int id, AttnUnit &u)
 {

@@ -19,7 +19,7 @@
 //
 // Measured, BF16, heads of 128: 32 sequences of one token over 146 k positions
 // in all, 32 heads on 8: 121 us for 596 MB, 4.9 TB/s, bound by HBM. One token
-// over 1000 positions, 8 heads on 1: 8.5 us a call, bound by round trips to
+// over 1000 positions, 8 heads on 1: 8.3 us a call, bound by round trips to
 // memory that follow one another (lengths, table, keys, join of 8 parts).
 #pragma once
 
@@ -353,9 +353,9 @@ __global__ __launch_bounds__(256, DIM * NB <= 256 && DIM < 256 ? 2 : 1) void att
     // splits the joins are joined the same way, each result in the slot of its
     // first split. A join thus reads at most kJoin slots, all loads in flight,
     // and always in split order: the result does not depend on who came last.
-    // (One token over 1000 positions: 9.7 us, with the second launch 12.4; 24
-    // rows x 16 sequences of up to 16384 positions: 24.7 to 39 us, with the
-    // second launch 20.)
+    // (When it was chosen: one token over 1000 positions 9.7 us, with the second
+    // launch 12.4; 24 rows x 16 sequences of up to 16384 positions 24.7 to 39
+    // us, with the second launch 20.)
     auto leave = [&](int r, f32x4 v, float m, float l) {
         int tok, head;
         row_place(a, u, u.row0 + r, tok, head);

@@ -1141,7 +1141,7 @@ const char *proj_strerror(int status)
     case PROJ_ERR_NOT_PREPARED: return "layer not prepared";
     case PROJ_ERR_UNSUPPORTED: return "kernel configuration not compiled or does not tile the layer";
     case PROJ_ERR_HIP: return "HIP runtime error";
-    case PROJ_ERR_DEVICE: return "current device differs from the layer's device";
+    case PROJ_ERR_DEVICE: return "current device differs from the layer's or the tensors'";
     case PROJ_ERR_SCRATCH: return "the plan's split-K partials exceed the fixed scratch of proj_run_noalloc";
     case PROJ_ERR_ARG: return "a size, stride, type or index is outside what the operator takes";
     case PROJ_ERR_PAGES: return "too few free pages in the pool";

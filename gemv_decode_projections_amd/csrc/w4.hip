@@ -5,7 +5,7 @@
 // bits or'ed to the end of an FP16 number are that number plus q units of its
 // last place, z comes off by one packed subtraction, and BF16 takes two more
 // operations on the bits (weight_operand; the conversion of signed nibbles
-// takes longer: 2304 x 8192, one token 7.3 us, this way 6.5). So an operand is
+// takes longer: 2304 x 8192, one token 7.3 us, this way 6.2). So an operand is
 // q - z itself, exact: an activation meets nothing else, be it an infinity or
 // an outlier on weights of zero. Products are exact, sums FP32, and the scale
 // multiplies the group's FP32 sum, so no weight is ever rounded.
@@ -14,9 +14,9 @@
 // weight byte). A workgroup owns RB blocks of 16 rows and 16 NT tokens; its
 // waves split K, each unit of 128 k is one 16-byte load per lane and row
 // block, 1 KB contiguous per wave. Measured, BF16: 2304 x 8192, groups of 128,
-// one token: 6.4 us (9.9 MB at 1.5 TB/s: 144 row blocks fill little over half
+// one token: 6.2 us (9.9 MB at 1.6 TB/s: 144 row blocks fill little over half
 // the card, and the time is a launch, two loads' latency, the operands and the
-// join of the waves); 8192 x 4096, groups of 64, 32 tokens: 9.8 us, bound by
+// join of the waves); 8192 x 4096, groups of 64, 32 tokens: 9.4 us, bound by
 // the activations that every workgroup reads from L2.
 #include <limits.h>
 

@@ -135,6 +135,8 @@ int blk_pool_compact(blk_pool *pool, int max_moves, int32_t *src, int32_t *dst);
  *       gate may be NULL.
  *   lse: NULL, or float32 tokens x heads (contiguous): ln sum_j exp(scale *
  *       q . K[j]), -inf for a token that sees nothing.
+ *   A value of infinity under a weight too small for the cache's type (2^-32
+ *   of the row's largest in FP16, 2^-126 in BF16) gives NaN.
  *   max_q: the largest number of new tokens of one sequence, which picks the
  *       kernel (any value >= 1 gives right results; the true one is fastest).
  *   ws: blk_attn_workspace_bytes(head_dim) bytes, 256-byte aligned, its first
