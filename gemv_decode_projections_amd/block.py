@@ -262,7 +262,8 @@ def attn_run(q, cache, table, q_start, kv_len, out, ws, *, max_q=None, scale=Non
     times sigmoid(gate) if given.
 
     A token sees the positions up to its own (the last `window` of them if window > 0); heads share
-    key heads in groups. Tokens of no sequence (from q_start[-1] on) are left as they are. lse (float32, tokens x heads) receives the log of the sums of exponentials.
+    key heads in groups. Tokens of no sequence (from q_start[-1] on) are left as they are. lse (float32,
+    tokens x heads) receives the log of the sums of exponentials.
     max_q is the largest number of new tokens of a sequence (default: all of them): it picks the
     kernel, not the result."""
     if ws.head_dim < cache.head_dim or ws.index != cache._index:

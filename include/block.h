@@ -14,8 +14,8 @@
  * kernels themselves, so no value in them makes a kernel leave its buffers.
  * Strides are in elements; the stride of a dimension with one entry is not
  * looked at. Rows that a call writes must not overlap (PROJ_ERR_ARG); those
- * that it only reads may. The library keeps no state between calls: what a call needs
- * beyond its tensors is a buffer of the caller.
+ * that it only reads may. The library keeps no state between calls: what a
+ * call needs beyond its tensors is a buffer of the caller.
  */
 #ifndef BLOCK_H
 #define BLOCK_H
